@@ -36,7 +36,7 @@
  *   - Errors are returned, never raised or aborted on. Errors found by a kernel
  *     (a wait that ran out, a gather index out of range) are recorded in the
  *     workspace and read with mhc_get_device_status.
- *   - Shapes: 1 <= R <= 128, H a multiple of 64 with H/64 <= 148 (H <= 9472),
+ *   - Shapes of the boundary entry points: 1 <= R <= 128, H a multiple of 64 with H/64 <= 148 (H <= 9472),
  *     n in {1, 2, 4}, 1 <= P <= 16, 1 <= k <= 16.
  *   - Alignment: bf16 tensors and fn 16-byte aligned, MXFP8 data 8-byte aligned,
  *     fp32 vectors 4-byte aligned; partial_stride a multiple of 8 elements.
@@ -321,6 +321,113 @@ MHC_API mhc_status mhc_coeffs(
  * and scale layouts as mhc_mxfp8_out. 1 <= R <= 65535, H a multiple of 32. */
 MHC_API mhc_status mxfp8_quantize_rows(const mhc_bf16* x, int rows, int hidden,
                                const mhc_mxfp8_out* out, mhc_stream stream);
+
+/* The products and the routing of a sublayer: what turns a boundary's layer
+ * input into the next boundary's shared_output, expert_weights,
+ * expanded_idx_to_permuted_idx and gemm2_permuted ([decode] SpecializedDecode.run:
+ * MoEStep; the pages name these steps and print none of their arithmetic).
+ * Rows are tokens; 1 <= rows <= 65535 here (a prompt's rows too, not only a
+ * decode batch's). The conventions above hold, with the dependent-launch rule for
+ * weights read as: mhc_linear requests `weight` and `weight_scale` before it waits
+ * for the kernel before it on the stream.
+ *
+ * mhc_linear: out[r, f] = act( sum_k x[r, k] weight[f, k] + bias[f] ) + residual[r, f]
+ *   x [rows, in] and weight [out, in] (contiguous) are bf16 (both scales NULL), or
+ *   both MXFP8: E4M3 bytes with E8M0 scales in the swizzled 128x4 layout of
+ *   mhc_mxfp8_out, padding bytes zero (as the boundaries and mxfp8_quantize_rows
+ *   write them). Accumulated in fp32; out is rounded once, to bf16, or fp32
+ *   (out_fp32 != 0). bias fp32 and residual bf16 may be NULL.
+ *   activation: MHC_ACT_NONE / RELU / SILU (v sigmoid(v)) / GELU (v Phi(v), exact);
+ *   MHC_ACT_SWIGLU: weight is [2 out, in] (bias [2 out]), gate rows first, and
+ *   act = silu(gate) * up.
+ *   Strides are in elements, between rows; x rows 16-byte aligned (x_stride a
+ *   multiple of 8 in bf16, 16 in MXFP8). residual may be out itself (same pointer
+ *   and stride; out then bf16); no other output may overlap an input.
+ *   in_features a multiple of 8 (bf16) or 32 (MXFP8), <= 65536; out_features <=
+ *   2^20, a multiple of 128 for MXFP8 with SWIGLU. x and weight 16-byte aligned,
+ *   scales 16-byte aligned.
+ *   workspace: mhc_linear_workspace_bytes(rows) bytes (a size for more rows serves
+ *   fewer), 256-byte aligned, zeroed once before first use (mhc_workspace_init),
+ *   used by one stream at a time; two graphs that may run at once need one each. A
+ *   workspace whose call recorded a device error is zeroed again before reuse. */
+typedef enum {
+  MHC_ACT_NONE = 0,
+  MHC_ACT_RELU = 1,
+  MHC_ACT_SILU = 2,
+  MHC_ACT_GELU = 3,
+  MHC_ACT_SWIGLU = 4
+} mhc_activation;
+
+MHC_API size_t mhc_linear_workspace_bytes(int rows);
+MHC_API mhc_status mhc_linear(
+    const void* x, const uint8_t* x_scale, int64_t x_stride, const void* weight, const uint8_t* weight_scale,
+    const float* bias, mhc_activation activation, const mhc_bf16* residual, int64_t residual_stride,
+    void* out, int out_fp32, int64_t out_stride, int rows, int in_features, int out_features,
+    void* workspace, size_t ws_bytes, mhc_stream stream);
+
+/* mhc_moe_route: the experts of each row and the permutation of the pairs
+ * (row, slot) by expert. Per row, from logits [rows, E] (fp32, or bf16 with
+ * logits_bf16 != 0):
+ *   score   softmax (MHC_SCORE_SOFTMAX) or sigmoid of the logits
+ *   choice  score + bias[e] (bias fp32, a balance bias that decides who is chosen
+ *           but not the weight); with bias NULL choices order as the logits
+ *   groups  E / num_groups consecutive experts each; a group's value is the sum of
+ *           its group_top largest (score + bias), and the top_groups groups of the
+ *           largest value stay. num_groups 1: all stay.
+ *   ids     the top_k largest choices of what stayed, in descending order; equal
+ *           choices (and groups) go to the lowest index
+ *   weights score of the chosen, divided by their sum when renormalize != 0, times
+ *           weight_scale
+ * Choices are compared as if score + bias were computed in 64 bits: near-equal
+ * scores do not depend on fp32 rounding. An expert whose logit or bias is -inf or
+ * NaN cannot be chosen and adds nothing to the softmax's sum when its logit is; a
+ * slot for which no expert is left has id -1, weight 0 and e2p -1 (the finalize
+ * adds nothing for it). A row whose logits are all -inf is so a padded row.
+ * Logits of +inf count as equal to one another and above all others.
+ * Outputs: expert_weights [rows, top_k] fp32, expert_ids [rows, top_k],
+ * expanded_idx_to_permuted_idx [rows*top_k], permuted_rows [rows*top_k]: the
+ * source row of each permuted row (-1 behind the last), expert_offsets [E + 1]:
+ * expert e owns the permuted rows [offsets[e], offsets[e+1]), its pairs in order
+ * of their expanded index. int32, all written in full.
+ * 1 <= E <= 1024, 1 <= top_k <= min(16, E), num_groups a divisor of E, at most 32,
+ * 1 <= top_groups <= num_groups, group_top 1 or 2. logits 4-byte aligned (2 for
+ * bf16), rows contiguous. workspace: as mhc_linear's. */
+typedef enum { MHC_SCORE_SOFTMAX = 0, MHC_SCORE_SIGMOID = 1 } mhc_score;
+
+typedef struct {
+  mhc_score score;
+  int num_groups;
+  int top_groups;
+  int group_top;
+  int top_k;
+  int renormalize;
+  float weight_scale;
+} mhc_route_args;
+
+MHC_API size_t mhc_moe_route_workspace_bytes(int rows, int experts, int top_k);
+MHC_API mhc_status mhc_moe_route(
+    const void* logits, int logits_bf16, const float* bias, const mhc_route_args* args, float* expert_weights,
+    int32_t* expert_ids, int32_t* expanded_idx_to_permuted_idx, int32_t* permuted_rows, int32_t* expert_offsets,
+    int rows, int experts, void* workspace, size_t ws_bytes, mhc_stream stream);
+
+/* mhc_moe_experts: the experts' products over the permuted rows of mhc_moe_route.
+ * For each permuted row q of expert e (expert_offsets), with v = x[permuted_rows[q]]:
+ *   inner = bf16( silu(w13[e, :I] v) * (w13[e, I:] v) ),  I = intermediate
+ *   gemm2_permuted[q] = bf16( w2[e] inner )
+ * x [rows, hidden] bf16 (x_stride elements between rows, a multiple of 8), w13
+ * [E, 2I, hidden] (gate rows first), w2 [E, hidden, I] bf16, contiguous; sums in
+ * fp32, the intermediate rounded to bf16 (the type the second product takes).
+ * num_permuted is the length of permuted_rows and of gemm2_permuted; rows at and
+ * behind expert_offsets[E] are not written. An entry of permuted_rows outside
+ * [0, rows) is read as row 0 and recorded as MHC_ERR_DEVICE_INDEX; offsets that
+ * decrease or leave [0, num_permuted] record it and nothing is computed.
+ * hidden and intermediate multiples of 8, <= 65536; E <= 1024; num_permuted <=
+ * 16 * 65535. workspace: as mhc_linear's; it also holds the intermediate rows. */
+MHC_API size_t mhc_moe_experts_workspace_bytes(int rows, int num_permuted, int intermediate);
+MHC_API mhc_status mhc_moe_experts(
+    const mhc_bf16* x, int64_t x_stride, const mhc_bf16* w13, const mhc_bf16* w2, const int32_t* permuted_rows,
+    const int32_t* expert_offsets, mhc_bf16* gemm2_permuted, int rows, int num_permuted, int experts, int hidden,
+    int intermediate, void* workspace, size_t ws_bytes, mhc_stream stream);
 
 /* mhc_boundary_post_pre for callers that cannot allocate device memory.
  * The pages have no counterpart: this entry point exists for callers such as a

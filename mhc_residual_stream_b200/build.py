@@ -21,8 +21,9 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmhc.so")
 STAMP = LIB + ".src-sha256"
 
-SOURCES = [os.path.join(CSRC, "mhc_boundary.cu")]
-HEADERS = [os.path.join(CSRC, "mhc_device.cuh"), os.path.join(INCLUDE, "mhc.h")]
+SOURCES = [os.path.join(CSRC, f) for f in ("mhc_boundary.cu", "mhc_gemm.cu", "mhc_route.cu")]
+HEADERS = [os.path.join(CSRC, f) for f in ("mhc_device.cuh", "mhc_host.cuh", "mhc_tcgen05.cuh")] + \
+    [os.path.join(INCLUDE, "mhc.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

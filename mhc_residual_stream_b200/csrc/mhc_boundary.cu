@@ -40,6 +40,7 @@
 
 #include "../../include/mhc.h"
 #include "mhc_device.cuh"
+#include "mhc_host.cuh"
 
 namespace mhc {
 
@@ -50,11 +51,8 @@ constexpr int kMaxRows = 128;
 constexpr int kMaxPartials = 16;
 constexpr int kMaxTopK = 16;
 constexpr int kMaxIters = 1000;
-constexpr int kMaxBlocks = 148;  // most H/64 blocks: the tail's per-lane loads are sized for it
 constexpr int kPrefetchRows = 64;  // the streaming kernel prefetches its rows into L2 up to this many
 constexpr int kPrefetchPartRows = 96;  // and its first kPrefetchRows rows up to this many
-// Workspace header: the status word (byte 0); the partial sums follow.
-constexpr size_t kWsHeader = 1024;
 constexpr int kStatusWord = 0;
 
 enum Front { kPartials = 0, kMoe = 1, kStreams = 2, kBroadcast = 3, kMailbox = 4 };
@@ -1259,11 +1257,6 @@ namespace {
 
 using namespace mhc;
 
-int64_t g_budget_ns = 1000000000LL;
-int g_extra_tx = 0;
-
-inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 size_t ws_layout(int R, int H, int n, size_t* sc2_off, size_t* dot_off) {
   const int G = H / kCols;
   const size_t a = kWsHeader;
@@ -1326,25 +1319,6 @@ mhc_status launch_pdl(Kern kern, int grid, int smem, cudaStream_t stream, const 
 
 // ---------------------------------------------------------------- tensor maps
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_tiled() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(f);
-    else
-      (void)cudaGetLastError();
-  });
-  return fn;
-}
-
 // A 3-D bf16 tensor map (innermost dimension first; strides in bytes of
 // dimensions 1 and 2), no swizzle, out-of-range elements read as zero.
 bool make_map3(CUtensorMap* m, const void* base, const uint64_t (&dims)[3], const uint64_t (&strides)[2],
@@ -1375,20 +1349,6 @@ bool staged_maps(const Params& p, CUtensorMap* maps) {
   const uint64_t rd[3] = {H, static_cast<uint64_t>(N), R}, rs[2] = {H * 2, H * 2 * N};
   const uint32_t rb[3] = {kCols, static_cast<uint32_t>(N), static_cast<uint32_t>(R)};
   return make_map3(&maps[0], p.pptr[0], pd, ps, pb) && make_map3(&maps[1], p.residual, rd, rs, rb);
-}
-
-// Number of SMs of the current device (cached per device; safe to call from
-// several host threads).
-int sm_count() {
-  static std::atomic<int> cached[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return kMaxBlocks;
-  int n = cached[dev].load(std::memory_order_relaxed);
-  if (n == 0) {
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return kMaxBlocks;
-    cached[dev].store(n, std::memory_order_relaxed);
-  }
-  return n;
 }
 
 // Raise a kernel's dynamic shared memory limit to 200 KB, once per device

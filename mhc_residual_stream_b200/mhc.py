@@ -8,7 +8,8 @@ fallback: without the built library every call raises.
 
 Shapes follow the C ABI: residual [R, n, H] bf16, partials [P, R, H] bf16 (any
 stride between partials), post [R, n], comb [R, n, n], pre [R, n] fp32,
-norm_weight [H] bf16, fn [n*H, 2n+n^2] fp32.
+norm_weight [H] bf16, fn [n*H, 2n+n^2] fp32. The sublayer entry points
+(mhc_linear, mhc_moe_route, mhc_moe_experts) take matrices [rows, features].
 """
 
 from __future__ import annotations
@@ -44,6 +45,16 @@ class CoeffArgs(ctypes.Structure):
 
 class Mxfp8Out(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("swizzled_128x4", ctypes.c_int)]
+
+
+class RouteArgs(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int), ("num_groups", ctypes.c_int), ("top_groups", ctypes.c_int),
+                ("group_top", ctypes.c_int), ("top_k", ctypes.c_int), ("renormalize", ctypes.c_int),
+                ("weight_scale", ctypes.c_float)]
+
+
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "swiglu": 4}
+SCORES = {"softmax": 0, "sigmoid": 1}
 
 
 @dataclass
@@ -117,6 +128,12 @@ def lib() -> ctypes.CDLL:
         "mhc_ipc_release": (_i, [_vp]),
         "mhc_projection_pack_bytes": (_sz, [_i, _i]),
         "mhc_projection_pack": (_i, [_vp, _vp, _i, _i, _vp]),
+        "mhc_linear_workspace_bytes": (_sz, [_i]),
+        "mhc_linear": (_i, [_vp, _vp, _i64, _vp, _vp, _vp, _i, _vp, _i64, _vp, _i, _i64, _i, _i, _i, _vp, _sz, _vp]),
+        "mhc_moe_route_workspace_bytes": (_sz, [_i, _i, _i]),
+        "mhc_moe_route": (_i, [_vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _vp, _sz, _vp]),
+        "mhc_moe_experts_workspace_bytes": (_sz, [_i, _i, _i]),
+        "mhc_moe_experts": (_i, [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _sz, _vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -483,6 +500,172 @@ def mxfp8_quantize_rows(x, data, scale, swizzled_128x4: bool = True, stream=None
     qs = _mxfp8_struct((data, scale, swizzled_128x4))
     st = lib().mxfp8_quantize_rows(_p(x), R, H, ctypes.byref(qs), _stream(stream))
     _check(st, "mxfp8_quantize_rows")
+
+
+# ------------------------------------------------------------------ sublayer products and routing
+
+def _here(t):
+    """The tensors of a sublayer call lie on the current device, whose stream it runs on."""
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {t.device}, current device cuda:{torch.cuda.current_device()}")
+
+
+def _with(first, *others):
+    _here(first)
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+
+
+def _workspace(n: int, where: str, device):
+    if n == 0:
+        raise MhcError(UNSUPPORTED_SHAPE, where)
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def _row_stride(t, name):
+    """The stride between the rows of a matrix whose rows are contiguous."""
+    R, C = t.shape
+    if C > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.stride(0) if R > 1 else (C + 15) // 16 * 16
+
+
+def mhc_linear_workspace_bytes(rows: int) -> int:
+    return int(lib().mhc_linear_workspace_bytes(rows))
+
+
+def new_linear_workspace(rows: int, device=None) -> torch.Tensor:
+    """A zeroed workspace of mhc_linear for up to `rows` rows."""
+    return _workspace(mhc_linear_workspace_bytes(rows), "mhc_linear_workspace_bytes", device)
+
+
+def _operand(v, name):
+    """(data, scale) of a bf16 matrix, or of an MXFP8 one given as (data, scale, swizzled)."""
+    if isinstance(v, torch.Tensor):
+        _need(v, torch.bfloat16, name, 2)
+        return v, None
+    data, scale, swizzled = v
+    _need(data, torch.uint8, name + " data", 2)
+    _need(scale, torch.uint8, name + " scale")
+    _contig(scale, name + " scale")
+    if not swizzled:
+        raise ValueError(f"{name} scales must be in the swizzled 128x4 layout")
+    if data.shape[1] % 32 == 0 and scale.numel() < mhc_mxfp8_scale_bytes(data.shape[0], data.shape[1], True):
+        raise ValueError(f"{name} scale needs {mhc_mxfp8_scale_bytes(data.shape[0], data.shape[1], True)} bytes")
+    return data, scale
+
+
+def mhc_linear(x, weight, out, bias=None, activation: str = "none", residual=None, workspace=None, stream=None):
+    """out [R, N] = activation(x [R, K] @ weight [N, K]^T + bias [N]) + residual [R, N].
+    x and weight are bf16, or both MXFP8 as (data, scale, True); out is bf16 or fp32.
+    activation: none, relu, silu, gelu, or swiglu (weight [2N, K], bias [2N]: gate rows,
+    then up rows). Rows of x, residual and out may be strided; residual may be out."""
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
+    xd, xs = _operand(x, "x")
+    wd, wsc = _operand(weight, "weight")
+    if (xs is None) != (wsc is None):
+        raise TypeError("x and weight must both be bf16 or both MXFP8")
+    _contig(wd, "weight")
+    fp32 = isinstance(out, torch.Tensor) and out.dtype == torch.float32
+    _need(out, torch.float32 if fp32 else torch.bfloat16, "out", 2)
+    _need(bias, torch.float32, "bias", 1)
+    _contig(bias, "bias")
+    _need(residual, torch.bfloat16, "residual", 2)
+    _with(xd, xs, wd, wsc, out, bias, residual, workspace)
+    R, K = xd.shape
+    N = out.shape[1]
+    W = 2 * N if activation == "swiglu" else N
+    if tuple(wd.shape) != (W, K) or out.shape[0] != R or (bias is not None and bias.shape[0] != W) \
+            or (residual is not None and tuple(residual.shape) != (R, N)):
+        raise ValueError("x/weight/bias/residual/out shapes disagree")
+    st = lib().mhc_linear(
+        _p(xd), _p(xs), _row_stride(xd, "x"), _p(wd), _p(wsc), _p(bias), ACTIVATIONS[activation], _p(residual),
+        0 if residual is None else _row_stride(residual, "residual"), _p(out), 1 if fp32 else 0,
+        _row_stride(out, "out"), R, K, N, _p(workspace), 0 if workspace is None else workspace.numel(),
+        _stream(stream))
+    _check(st, "mhc_linear")
+
+
+def mhc_moe_route_workspace_bytes(rows: int, experts: int, top_k: int) -> int:
+    return int(lib().mhc_moe_route_workspace_bytes(rows, experts, top_k))
+
+
+def new_moe_route_workspace(rows: int, experts: int, top_k: int, device=None) -> torch.Tensor:
+    """A zeroed workspace of mhc_moe_route."""
+    return _workspace(mhc_moe_route_workspace_bytes(rows, experts, top_k), "mhc_moe_route_workspace_bytes", device)
+
+
+def mhc_moe_route(logits, expert_weights, expert_ids, expanded_idx_to_permuted_idx, permuted_rows, expert_offsets,
+                  bias=None, scoring: str = "softmax", num_groups: int = 1, top_groups: int = 1, group_top: int = 1,
+                  renormalize: bool = True, weight_scale: float = 1.0, workspace=None, stream=None):
+    """Experts of each row of logits [R, E] (fp32 or bf16) and the permutation of the
+    (row, slot) pairs by expert: expert_weights [R, k] fp32, expert_ids [R, k],
+    expanded_idx_to_permuted_idx [R*k], permuted_rows [R*k], expert_offsets [E+1] int32."""
+    if scoring not in SCORES:
+        raise ValueError(f"scoring must be one of {sorted(SCORES)}")
+    bf16 = isinstance(logits, torch.Tensor) and logits.dtype == torch.bfloat16
+    _need(logits, torch.bfloat16 if bf16 else torch.float32, "logits", 2)
+    _need(bias, torch.float32, "bias", 1)
+    _need(expert_weights, torch.float32, "expert_weights", 2)
+    _need(expert_ids, torch.int32, "expert_ids", 2)
+    for t, n in ((expanded_idx_to_permuted_idx, "expanded_idx_to_permuted_idx"), (permuted_rows, "permuted_rows"),
+                 (expert_offsets, "expert_offsets")):
+        _need(t, torch.int32, n, 1)
+    for t, n in ((logits, "logits"), (bias, "bias"), (expert_weights, "expert_weights"), (expert_ids, "expert_ids"),
+                 (expanded_idx_to_permuted_idx, "expanded_idx_to_permuted_idx"), (permuted_rows, "permuted_rows"),
+                 (expert_offsets, "expert_offsets")):
+        _contig(t, n)
+    _with(logits, bias, expert_weights, expert_ids, expanded_idx_to_permuted_idx, permuted_rows, expert_offsets,
+          workspace)
+    R, E = logits.shape
+    k = expert_weights.shape[1]
+    if expert_weights.shape[0] != R or tuple(expert_ids.shape) != (R, k) \
+            or expanded_idx_to_permuted_idx.shape[0] != R * k or permuted_rows.shape[0] != R * k \
+            or expert_offsets.shape[0] != E + 1 or (bias is not None and bias.shape[0] != E):
+        raise ValueError("MoE route shapes disagree")
+    a = RouteArgs(SCORES[scoring], int(num_groups), int(top_groups), int(group_top), k, 1 if renormalize else 0,
+                  float(weight_scale))
+    st = lib().mhc_moe_route(
+        _p(logits), 1 if bf16 else 0, _p(bias), ctypes.byref(a), _p(expert_weights), _p(expert_ids),
+        _p(expanded_idx_to_permuted_idx), _p(permuted_rows), _p(expert_offsets), R, E, _p(workspace),
+        0 if workspace is None else workspace.numel(), _stream(stream))
+    _check(st, "mhc_moe_route")
+
+
+def mhc_moe_experts_workspace_bytes(rows: int, num_permuted: int, intermediate: int) -> int:
+    return int(lib().mhc_moe_experts_workspace_bytes(rows, num_permuted, intermediate))
+
+
+def new_moe_experts_workspace(rows: int, num_permuted: int, intermediate: int, device=None) -> torch.Tensor:
+    """A zeroed workspace of mhc_moe_experts."""
+    return _workspace(mhc_moe_experts_workspace_bytes(rows, num_permuted, intermediate),
+                      "mhc_moe_experts_workspace_bytes", device)
+
+
+def mhc_moe_experts(x, w13, w2, permuted_rows, expert_offsets, gemm2_permuted, workspace=None, stream=None):
+    """gemm2_permuted [P, H] of the permuted rows: w2[e] (silu(gate) * up) with gate and up
+    from w13[e] [2I, H] and the rows x[permuted_rows], expert by expert (expert_offsets)."""
+    _need(x, torch.bfloat16, "x", 2)
+    _need(w13, torch.bfloat16, "w13", 3)
+    _need(w2, torch.bfloat16, "w2", 3)
+    _need(permuted_rows, torch.int32, "permuted_rows", 1)
+    _need(expert_offsets, torch.int32, "expert_offsets", 1)
+    _need(gemm2_permuted, torch.bfloat16, "gemm2_permuted", 2)
+    for t, n in ((w13, "w13"), (w2, "w2"), (permuted_rows, "permuted_rows"), (expert_offsets, "expert_offsets"),
+                 (gemm2_permuted, "gemm2_permuted")):
+        _contig(t, n)
+    _with(x, w13, w2, permuted_rows, expert_offsets, gemm2_permuted, workspace)
+    R, H = x.shape
+    E, I, P = w2.shape[0], w2.shape[2], permuted_rows.shape[0]
+    if tuple(w13.shape) != (E, 2 * I, H) or w2.shape[1] != H or expert_offsets.shape[0] != E + 1 \
+            or tuple(gemm2_permuted.shape) != (P, H):
+        raise ValueError("MoE experts shapes disagree")
+    st = lib().mhc_moe_experts(
+        _p(x), _row_stride(x, "x"), _p(w13), _p(w2), _p(permuted_rows), _p(expert_offsets), _p(gemm2_permuted), R, P,
+        E, H, I, _p(workspace), 0 if workspace is None else workspace.numel(), _stream(stream))
+    _check(st, "mhc_moe_experts")
 
 
 def mhc_status_string(status: int) -> str:

@@ -130,13 +130,14 @@ def build_stamped(out_dir: str | None = None) -> str:
     os.makedirs(out_dir, exist_ok=True)
     with open(build.SOURCES[0]) as f:
         src = instrument(f.read())
-    src = src.replace('#include "mhc_device.cuh"', '#include "%s"' % os.path.join(build.CSRC, "mhc_device.cuh"))
+    for h in ("mhc_device.cuh", "mhc_host.cuh"):
+        src = src.replace('#include "%s"' % h, '#include "%s"' % os.path.join(build.CSRC, h))
     src = src.replace('#include "../../include/mhc.h"', '#include "%s"' % os.path.join(build.INCLUDE, "mhc.h"))
     cu = os.path.join(out_dir, "mhc_boundary_stamped.cu")
     with open(cu, "w") as f:
         f.write(src)
     lib = os.path.join(out_dir, "libmhc.so")
-    res = subprocess.run([build._nvcc(), *build.NVCC_FLAGS, "-I", build.INCLUDE, "-o", lib, cu],
+    res = subprocess.run([build._nvcc(), *build.NVCC_FLAGS, "-I", build.INCLUDE, "-o", lib, cu, *build.SOURCES[1:]],
                          capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"nvcc failed ({res.returncode}):\n{res.stderr}")

@@ -1,4 +1,4 @@
-"""CPU oracle of the mHC decode boundary.
+"""CPU oracle of the mHC decode boundary and of the sublayer operators.
 
 TEST INFRASTRUCTURE ONLY. This package is a plain, slow float64 restatement
 of what the boundary computes. It exists to check the CUDA library and to be
@@ -14,3 +14,4 @@ result rests on a convention that no independent value can fix carry the words
 """
 
 from .mhc import *  # noqa: F401,F403
+from .sublayer import *  # noqa: F401,F403

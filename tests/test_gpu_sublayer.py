@@ -1,0 +1,437 @@
+"""GPU tests of the sublayer operators (mhc_linear, mhc_moe_route,
+mhc_moe_experts) against the float64 oracle, at the bounds derived in
+tests/_sublayer.py."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from mhc_residual_stream_b200 import mhc as M
+
+from _sublayer import (DEV, assert_within, bf, draw_experts, experts_bound, f64, gen, i32, linear_bound, mxfp8,
+                       run_linear, run_route)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from mhc_residual_stream_b200 import build
+    build.build()
+    M.lib()
+    yield
+
+
+# ---------------------------------------------------------------- linear
+
+LINEAR = [  # rows, K, N, activation, bias, residual, out
+    (1, 8, 1, "none", False, False, torch.bfloat16),
+    (1, 7168, 256, "none", False, False, torch.float32),
+    (1, 64, 128, "silu", True, True, torch.bfloat16),
+    (2, 72, 129, "relu", True, False, torch.float32),
+    (3, 1000, 333, "gelu", True, True, torch.bfloat16),
+    (16, 512, 1000, "none", True, True, torch.float32),
+    (17, 136, 77, "swiglu", True, True, torch.bfloat16),
+    (32, 7168, 256, "none", False, False, torch.float32),
+    (33, 2048, 640, "swiglu", False, False, torch.float32),
+    (77, 1000, 333, "gelu", True, True, torch.float32),
+    (128, 256, 200, "swiglu", True, False, torch.bfloat16),
+    (129, 264, 130, "swiglu", True, True, torch.bfloat16),
+    (200, 520, 300, "silu", False, True, torch.bfloat16),
+    (257, 128, 257, "none", True, True, torch.bfloat16),
+    (300, 24, 2000, "relu", False, False, torch.bfloat16),
+    (1030, 192, 1100, "none", False, True, torch.float32),
+    (4099, 64, 64, "gelu", True, False, torch.bfloat16),
+]
+
+
+@pytest.mark.parametrize("R,K,N,act,bias,res,out", LINEAR)
+def test_linear_bf16(R, K, N, act, bias, res, out):
+    g = gen(R * 7 + K)
+    W = 2 * N if act == "swiglu" else N
+    x, w = bf((R, K), g), bf((W, K), g, 1.5 / K ** 0.5)
+    b = torch.randn(W, generator=g) * 0.3 if bias else None
+    r = bf((R, N), g) if res else None
+    got = run_linear(x.to(DEV), w.to(DEV), None if b is None else b.to(DEV), act, None if r is None else r.to(DEV), out)
+    exact, bound = linear_bound(f64(x), f64(w), None if b is None else f64(b), act, None if r is None else f64(r), out)
+    assert_within(got, exact, bound, f"linear {R}x{K}x{N} {act}")
+
+
+@pytest.mark.parametrize("R,K,N,act,bias,res,out", [
+    (1, 32, 1, "none", False, False, torch.float32),
+    (1, 7168, 512, "none", False, False, torch.bfloat16),
+    (5, 96, 200, "silu", True, True, torch.float32),
+    (64, 1024, 384, "swiglu", True, False, torch.bfloat16),
+    (100, 416, 333, "gelu", True, True, torch.bfloat16),
+    (128, 2048, 128, "none", False, True, torch.float32),
+    (129, 160, 256, "swiglu", False, True, torch.float32),
+    (300, 512, 700, "relu", True, False, torch.bfloat16),
+])
+def test_linear_mxfp8(R, K, N, act, bias, res, out):
+    g = gen(R * 11 + K)
+    W = 2 * N if act == "swiglu" else N
+    xv = torch.randn(R, K, generator=g) * torch.exp2(torch.randint(-4, 5, (R, 1), generator=g).float())
+    xd, xs, x = mxfp8(xv)
+    wd, wsc, w = mxfp8(torch.randn(W, K, generator=g) * (1.5 / K ** 0.5))
+    b = torch.randn(W, generator=g) * 0.3 if bias else None
+    r = bf((R, N), g) if res else None
+    got = run_linear((xd.to(DEV), xs.to(DEV), True), (wd.to(DEV), wsc.to(DEV), True), None if b is None else b.to(DEV),
+                     act, None if r is None else r.to(DEV), out)
+    exact, bound = linear_bound(x, w, None if b is None else f64(b), act, None if r is None else f64(r), out)
+    assert_within(got, exact, bound, f"mxfp8 linear {R}x{K}x{N} {act}")
+
+
+def test_linear_takes_what_the_quantizer_writes():
+    g = gen(3)
+    x, w = bf((70, 384), g), bf((256, 384), g, 0.1)
+    ops = []
+    for t in (x, w):
+        d = torch.empty(t.shape, dtype=torch.uint8, device=DEV)
+        s = torch.empty(M.mhc_mxfp8_scale_bytes(*t.shape, True), dtype=torch.uint8, device=DEV)
+        M.mxfp8_quantize_rows(t.to(DEV), d, s, True)
+        ops.append((d, s, True))
+    got = run_linear(*ops)
+    exact, bound = linear_bound(mxfp8(x.float())[2], mxfp8(w.float())[2], None, "none", None, torch.bfloat16)
+    assert_within(got, exact, bound, "quantized operands")
+
+
+def test_linear_strided_rows_and_untouched_surroundings():
+    g = gen(4)
+    xb, rb = bf((37, 208), g).to(DEV), bf((37, 90), g).to(DEV)
+    x, res = xb[:, 8:8 + 136], rb[:, 3:3 + 75]
+    w = bf((75, 136), g, 0.1).to(DEV)
+    ob = torch.full((40, 101), 7.0, dtype=torch.bfloat16, device=DEV)
+    run_linear(x, w, residual=res, out=ob[1:38, 5:80])
+    exact, bound = linear_bound(f64(x), f64(w), None, "none", f64(res), torch.bfloat16)
+    assert_within(ob[1:38, 5:80], exact, bound, "strided")
+    ob[1:38, 5:80] = 7.0
+    assert bool((ob == 7.0).all())
+
+
+@pytest.mark.parametrize("R,N", [(5, 200), (130, 700)])
+def test_linear_residual_in_place(R, N):
+    g = gen(5)
+    x, w, r = bf((R, 512), g), bf((N, 512), g, 0.1), bf((R, N), g)
+    out = r.to(DEV)
+    run_linear(x.to(DEV), w.to(DEV), residual=out, out=out)
+    exact, bound = linear_bound(f64(x), f64(w), None, "none", f64(r), torch.bfloat16)
+    assert_within(out, exact, bound, "in place")
+
+
+def test_linear_nan_and_inf_stay_in_their_row_and_feature():
+    g = gen(6)
+    x, w = bf((20, 640), g), bf((300, 640), g, 0.05)
+    x[3, 17] = float("nan")
+    x[7, 600] = float("inf")
+    clean = run_linear(bf((20, 640), gen(6)).to(DEV), w.to(DEV))
+    w2 = w.clone()
+    w2[250, 5] = float("nan")
+    got = run_linear(x.to(DEV), w2.to(DEV))
+    assert bool(got[3].isnan().all()) and bool(got[:, 250].isnan().all())
+    keep = [r for r in range(20) if r not in (3, 7)]
+    cols = [c for c in range(300) if c != 250]
+    assert torch.equal(got[keep][:, cols], clean[keep][:, cols])
+    assert not bool(got[7, cols].isfinite().any())
+
+
+def test_linear_is_reproducible_and_its_workspace_serves_fewer_rows():
+    g = gen(8)
+    ws = M.new_linear_workspace(300, DEV)
+    w = bf((400, 4096), g, 0.02).to(DEV)
+    for R in (300, 1, 40, 300, 129):  # shared tiles in every one of them
+        x = bf((R, 4096), g).to(DEV)
+        a = run_linear(x, w, workspace=ws)
+        for _ in range(5):
+            assert torch.equal(a, run_linear(x, w, workspace=ws))
+        assert M.mhc_get_device_status(ws) == M.OK
+
+
+def test_linear_on_a_side_stream_and_in_a_graph():
+    g = gen(9)
+    x, w = bf((24, 1024), g).to(DEV), bf((512, 1024), g, 0.05).to(DEV)
+    want = run_linear(x, w)
+    s = torch.cuda.Stream()
+    ws, out = M.new_linear_workspace(24, DEV), torch.empty(24, 512, dtype=torch.bfloat16, device=DEV)
+    torch.cuda.synchronize()
+    M.mhc_linear(x, w, out, workspace=ws, stream=s)
+    s.synchronize()
+    assert torch.equal(out, want)
+    graphs = []
+    for _ in range(2):  # two graphs, a workspace each, replayed at once on two streams
+        ws, out = M.new_linear_workspace(24, DEV), torch.zeros(24, 512, dtype=torch.bfloat16, device=DEV)
+        gr = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(gr):
+            for _ in range(3):
+                M.mhc_linear(x, w, out, workspace=ws)
+        graphs.append((gr, ws, out, torch.cuda.Stream()))
+    for seed in (10, 11):
+        x.copy_(bf((24, 1024), gen(seed)))
+        torch.cuda.synchronize()
+        for gr, _, _, st in graphs:
+            with torch.cuda.stream(st):
+                gr.replay()
+        torch.cuda.synchronize()
+        want = run_linear(x, w)
+        for _, _, out, _ in graphs:
+            assert torch.equal(out, want)
+
+
+def test_linear_wait_that_runs_out_is_reported():
+    g = gen(12)
+    x, w = bf((8, 512), g).to(DEV), bf((256, 512), g, 0.05).to(DEV)
+    want = run_linear(x, w)
+    ws = M.new_linear_workspace(8, DEV)
+    torch.cuda.synchronize()
+    old = M.mhc_debug_set_wait(2_000_000, 4)
+    try:
+        run_linear(x, w, workspace=ws)
+        assert M.mhc_get_device_status(ws) == M.DEVICE_TIMEOUT
+    finally:
+        M.mhc_debug_set_wait(old, 0)
+    M.mhc_workspace_init(ws)
+    assert torch.equal(run_linear(x, w, workspace=ws), want)
+    assert M.mhc_get_device_status(ws) == M.OK
+
+
+# ---------------------------------------------------------------- routing
+
+def check_route(logits, k, bias=None, **kw):
+    got = run_route(logits.to(DEV), k, None if bias is None else bias.to(DEV), **kw)
+    w, ids, e2p, prow, off = [t.cpu() for t in got]
+    ow, oids = O.moe_route(f64(logits), k, None if bias is None else f64(bias), **kw)
+    oe2p, oprow, ooff = O.moe_permute(oids, logits.shape[1])
+    assert np.array_equal(ids.numpy(), oids), "ids"
+    assert np.array_equal(off.numpy(), ooff), "offsets"
+    assert np.array_equal(e2p.numpy(), oe2p), "e2p"
+    assert np.array_equal(prow.numpy(), oprow), "permuted rows"
+    # scores by expf (2 steps) of an argument off by half a step of a range of at most
+    # twice the largest finite logit, sums of up to 1024 terms by tree (10 levels), two divisions
+    fin = logits.float()[logits.float().abs() < 1e3]
+    span = float(fin.abs().max()) if fin.numel() else 0.0
+    rel = (40 + 4 * span) * 2.0 ** -24
+    assert np.all(np.abs(f64(w) - ow) <= rel * np.abs(ow) + 2.0 ** -126), "weights"
+    return ow, oids
+
+
+@pytest.mark.parametrize("R", [1, 2, 16, 17, 100, 128, 129, 700, 3001])
+@pytest.mark.parametrize("E,k", [(64, 8), (200, 6)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_route_rows(R, E, k, scoring):
+    g = gen(R + E)
+    logits = torch.randn(R, E, generator=g) * 2
+    check_route(logits, k, scoring=scoring, renormalize=R % 2 == 0, weight_scale=2.5)
+
+
+@pytest.mark.parametrize("E,k,G,tg,gt", [
+    (1, 1, 1, 1, 1), (7, 7, 1, 1, 1), (7, 3, 7, 3, 2), (33, 16, 3, 2, 2), (96, 4, 32, 5, 1), (256, 8, 8, 4, 2),
+    (500, 12, 4, 1, 2), (512, 16, 1, 1, 1), (1000, 16, 8, 3, 2), (1024, 16, 32, 32, 1), (17, 1, 17, 17, 1),
+])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True])
+def test_route_shapes_and_groups(E, k, G, tg, gt, scoring, biased):
+    for R in (5, 150):
+        g = gen(E * 3 + R)
+        logits = torch.randn(R, E, generator=g) * 1.5
+        bias = torch.randn(E, generator=g) * 0.2 if biased else None
+        check_route(logits, k, bias, scoring=scoring, num_groups=G, top_groups=tg, group_top=gt,
+                    renormalize=biased)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("G", [1, 4])
+def test_route_unavailable_experts_and_rows(scoring, biased, G):
+    g = gen(77)
+    R, E, k = 140, 40, 6
+    logits = torch.randn(R, E, generator=g)
+    bias = torch.randn(E, generator=g) * 0.1 if biased else None
+    if biased:
+        bias[4] = -math.inf
+    logits[3] = -math.inf                       # nothing to choose
+    logits[5, 2:] = -math.inf                   # fewer than k
+    logits[6, 10:20] = -math.inf                # a whole group
+    logits[7, 9] = float("nan")
+    logits[8] = float("nan")
+    logits[9, 11] = math.inf
+    logits[10, [1, 30]] = math.inf
+    logits[11] = torch.finfo(torch.float32).min
+    logits[12] = -200.0 + torch.arange(E) * 0.5  # scores far below fp32's range
+    logits[120:] = -math.inf                    # padding
+    ow, ids = check_route(logits, k, bias, scoring=scoring, num_groups=G, top_groups=max(1, G // 2), group_top=2)
+    assert (ids[3] == -1).all() and (ids[120:] == -1).all() and (ids[5] >= 0).sum() == (2 if G else 0)
+    # no pair at all
+    check_route(torch.full((9, 12), -math.inf), 3, scoring=scoring)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_route_ties_go_to_the_lowest_index(scoring):
+    R, E = 64, 96
+    g = gen(5)
+    logits = torch.randint(0, 3, (R, E), generator=g).float()
+    logits[0] = 0.0
+    logits[1, ::2] = -0.0
+    bias = torch.randint(0, 2, (E,), generator=g).float()
+    for G, tg in ((1, 1), (8, 3)):
+        check_route(logits, 8, None, scoring=scoring, num_groups=G, top_groups=tg, group_top=2)
+        check_route(logits, 8, bias, scoring=scoring, num_groups=G, top_groups=tg, group_top=2)
+
+
+def test_route_near_equal_choices_do_not_depend_on_fp32_rounding():
+    # choices that differ by far less than fp32 resolves: neighbouring logits at the flat
+    # end of the sigmoid, under a common bias
+    R, E = 40, 64
+    g = gen(6)
+    base = 8.0 + torch.rand(R, 1, generator=g)
+    step = 2.0 ** -20 * torch.stack([torch.randperm(E, generator=g) for _ in range(R)]).float()
+    check_route(base + step, 8, torch.ones(E), scoring="sigmoid")
+    check_route(base + step, 8, torch.ones(E), scoring="softmax")
+
+
+def test_route_bf16_logits():
+    g = gen(13)
+    logits = bf((130, 256), g, 2.0)
+    check_route(logits, 8, torch.randn(256, generator=g) * 0.1, scoring="sigmoid", num_groups=8, top_groups=4,
+                group_top=2)
+    check_route(logits, 8, scoring="softmax")
+
+
+def test_route_reuses_its_workspace_and_is_captured():
+    g = gen(14)
+    ws = M.new_moe_route_workspace(2000, 128, 8, DEV)
+    for R in (2000, 3, 128, 900):
+        logits = torch.randn(R, 128, generator=g).to(DEV)
+        a = run_route(logits, 8, workspace=ws)
+        for _ in range(3):
+            assert all(torch.equal(p, q) for p, q in zip(a, run_route(logits, 8, workspace=ws)))
+    for R in (60, 900):
+        logits = torch.randn(R, 128, generator=g).to(DEV)
+        outs = run_route(logits, 8, workspace=ws)
+        gr = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(gr):
+            M.mhc_moe_route(logits, *outs, workspace=ws)
+        logits.copy_(torch.randn(R, 128, generator=g))
+        gr.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(outs, run_route(logits, 8)))
+
+
+# ---------------------------------------------------------------- experts
+
+def run_experts(x, w13, w2, prow, off, out=None, workspace=None):
+    P, I = len(prow), w2.shape[2]
+    out = torch.full((P, x.shape[1]), 5.0, dtype=torch.bfloat16, device=DEV) if out is None else out
+    ws = M.new_moe_experts_workspace(x.shape[0], P, I, DEV) if workspace is None else workspace
+    M.mhc_moe_experts(x.to(DEV), w13.to(DEV), w2.to(DEV), i32(prow), i32(off), out, workspace=ws)
+    return out, ws
+
+
+@pytest.mark.parametrize("R,k,E,H,I", [
+    (1, 1, 1, 8, 8), (1, 8, 64, 256, 128), (1, 2, 4, 2048, 136), (7, 3, 5, 72, 40), (16, 4, 16, 512, 264),
+    (37, 3, 24, 712, 328), (50, 8, 8, 192, 200), (128, 8, 32, 320, 72), (200, 2, 3, 136, 304), (700, 4, 6, 64, 128),
+    (20, 2, 300, 64, 16), (9, 16, 1000, 64, 8),
+])
+def test_experts(R, k, E, H, I):
+    x, w13, w2, e2p, prow, off = draw_experts(R, k, E, H, I, seed=R + E)
+    out, ws = run_experts(x, w13, w2, prow, off)
+    exact, bound = experts_bound(f64(x), f64(w13), f64(w2), prow, off)
+    assert_within(out, exact, bound, f"experts {R} {k} {E} {H} {I}")
+    again, _ = run_experts(x, w13, w2, prow, off, workspace=ws)
+    assert torch.equal(out, again) and M.mhc_get_device_status(ws) == M.OK
+
+
+@pytest.mark.parametrize("R,k", [(40, 4), (300, 2)])
+def test_experts_of_one_popular_expert_and_unused_places(R, k):
+    E, H, I = 12, 200, 136
+    ids = np.full((R, k), -1)
+    ids[:, 0] = 5                         # every row to one expert
+    ids[::3, 1] = 11
+    x, w13, w2, e2p, prow, off = draw_experts(R, k, E, H, I, seed=R, ids=ids)
+    out, ws = run_experts(x, w13, w2, prow, off)
+    used = int(off[-1])
+    assert used == R + (R + 2) // 3 < R * k
+    exact, bound = experts_bound(f64(x), f64(w13), f64(w2), prow, off)
+    assert_within(out[:used], exact[:used], bound[:used], "popular expert")
+    assert bool((out[used:] == 5.0).all())  # places behind the last pair are left as they were
+    none = run_experts(x, w13, w2, np.full(R * k, -1), np.zeros(E + 1))[0]
+    assert bool((none == 5.0).all())
+
+
+def test_experts_strided_rows():
+    x, w13, w2, e2p, prow, off = draw_experts(30, 2, 6, 128, 64, seed=2)
+    wide = torch.zeros(30, 152, dtype=torch.bfloat16, device=DEV)
+    wide[:, 16:144] = x.to(DEV)
+    out, _ = run_experts(wide[:, 16:144], w13, w2, prow, off)
+    assert torch.equal(out, run_experts(x, w13, w2, prow, off)[0])
+
+
+def test_experts_report_bad_indices():
+    x, w13, w2, e2p, prow, off = draw_experts(30, 2, 6, 128, 64, seed=3)
+    good, _ = run_experts(x, w13, w2, prow, off)
+    for bad in (30, -1, 1 << 30):  # a row that x does not have reads row 0
+        p = prow.copy()
+        p[11] = bad
+        out, ws = run_experts(x, w13, w2, p, off)
+        assert M.mhc_get_device_status(ws) == M.DEVICE_INDEX
+        keep = [i for i in range(60) if i != 11]
+        assert torch.equal(out[keep], good[keep])
+    for o in ([0, 10, 5, 20, 30, 40, 60], [0, 10, 20, 30, 40, 50, 61], [-1, 10, 20, 30, 40, 50, 60]):
+        out, ws = run_experts(x, w13, w2, prow, np.array(o))  # nothing is computed
+        assert M.mhc_get_device_status(ws) == M.DEVICE_INDEX
+        assert bool((out == 5.0).all())
+
+
+# ---------------------------------------------------------------- a run of them together
+
+@pytest.mark.parametrize("R,padded", [(1, 0), (24, 5), (128, 0)])
+def test_moe_sublayer_between_two_boundaries(R, padded):
+    """Router logits, routing, the experts, the shared expert, and the boundary that
+    finalizes them, against the oracle on what the library wrote stage by stage."""
+    from mhc_residual_stream_b200 import synthetic as S
+    H, I, E, k, n = 512, 192, 16, 4, 4
+    g = gen(R)
+    x = bf((R, H), g)
+    router, w13, w2 = bf((E, H), g, 0.1), bf((E, 2 * I, H), g, 0.06), bf((E, H, I), g, 0.1)
+    s13, s2 = bf((2 * I, H), g, 0.06), bf((H, I), g, 0.1)
+    bias = torch.randn(E, generator=g) * 0.1
+    d = S.draw_boundary(R, H, n=n, partials=1, seed=R)
+    t = {q: d[q].to(DEV) for q in ("residual", "post", "comb", "pre", "norm_weight")}
+    logits = run_linear(x.to(DEV), router.to(DEV), out_type=torch.float32)
+    if padded:
+        logits[R - padded:] = -math.inf
+    w, ids, e2p, prow, off = run_route(logits, k, bias.to(DEV), scoring="sigmoid", num_groups=4, top_groups=2,
+                                       group_top=2, weight_scale=2.0)
+    perm = torch.zeros(R * k, H, dtype=torch.bfloat16, device=DEV)
+    M.mhc_moe_experts(x.to(DEV), w13.to(DEV), w2.to(DEV), prow, off, perm,
+                      workspace=M.new_moe_experts_workspace(R, R * k, I, DEV))
+    inner = run_linear(x.to(DEV), s13.to(DEV), act="swiglu")
+    shared = run_linear(inner, s2.to(DEV))
+    res, li = torch.empty_like(t["residual"]), torch.empty(R, H, dtype=torch.bfloat16, device=DEV)
+    ws = M.new_workspace(R, H, n, DEV)
+    M.mhc_boundary_moe_finalize(perm, w, e2p, shared, t["residual"], t["post"], t["comb"], t["pre"], t["norm_weight"],
+                                1e-6, None, res, layer_input=li, workspace=ws)
+    assert M.mhc_get_device_status(ws) == M.OK
+    # stage by stage
+    ex, bd = linear_bound(f64(x), f64(router), None, "none", None, torch.float32)
+    live = R - padded
+    assert_within(logits[:live], ex[:live], bd[:live], "router logits")
+    ow, oids = O.moe_route(f64(logits), k, f64(bias), "sigmoid", 4, 2, 2, True, 2.0)
+    oe2p, oprow, ooff = O.moe_permute(oids, E)
+    assert np.array_equal(e2p.cpu().numpy(), oe2p) and np.array_equal(off.cpu().numpy(), ooff)
+    used = int(ooff[-1])
+    ex, bd = experts_bound(f64(x), f64(w13), f64(w2), oprow, ooff)
+    assert_within(perm[:used], ex[:used], bd[:used], "experts")
+    ex, bd = linear_bound(f64(inner), f64(s2), None, "none", None, torch.bfloat16)
+    assert_within(shared, ex, bd, "shared expert")
+    # the finalize: x = shared + sum_t w gemm2[e2p], padded rows the shared output alone
+    xs = f64(shared).copy()
+    for i, q in enumerate(oe2p):
+        if q >= 0:
+            xs[i // k] += f64(w).reshape(-1)[i] * f64(perm)[q]
+    want = O.post_mix(f64(d["residual"]), xs, f64(d["post"]), f64(d["comb"]))
+    # both sides rounded once; fp32 sums of terms of order one
+    assert np.all(np.abs(f64(res) - want) <= 2.0 ** -7 * np.abs(want) + 2.0 ** -16)
