@@ -22,7 +22,7 @@ LIB = os.path.join(HERE, "libmhc.so")
 STAMP = LIB + ".src-sha256"
 
 SOURCES = [os.path.join(CSRC, f) for f in ("mhc_boundary.cu", "mhc_gemm.cu", "mhc_route.cu")]
-HEADERS = [os.path.join(CSRC, f) for f in ("mhc_device.cuh", "mhc_host.cuh", "mhc_tcgen05.cuh")] + \
+HEADERS = [os.path.join(CSRC, f) for f in ("mhc_device.cuh", "mhc_host.cuh", "mhc_pair.cuh", "mhc_tcgen05.cuh")] + \
     [os.path.join(INCLUDE, "mhc.h")]
 
 NVCC_FLAGS = [

@@ -14,12 +14,17 @@
 //              tiles are copied to tensor memory beside them);
 //   warps 2-5  read a finished accumulator (a thread owns one output feature)
 //              and write act(acc + bias) + residual.
-// Tiles: as many full waves as there are take whole tiles; the rest is divided
-// evenly over the CTAs along the flattened (tile, K) axis, so a product of few
-// tiles still reads its weights with every SM. A tile shared by several CTAs is
-// joined by whichever of them finishes last: all write their fp32 sums to the
-// workspace and count up; the last adds them in K order (the result does not
-// depend on who is last) and runs the epilogue. Nobody waits for anybody.
+// Dividing the work. A product of at least a tile per SM gives whole tiles to
+// its persistent CTAs. A dense product of fewer divides each tile's K over a
+// cluster of up to 8 CTAs, which add their accumulators through distributed
+// shared memory, each its share of the token columns. The experts' products,
+// whose tiles only the device knows, divide the tiles that are left after the
+// full waves evenly over all CTAs along the flattened (tile, K) axis when a tile
+// has few token columns; a tile shared by several CTAs is joined by whichever of
+// them finishes last: all write their fp32 sums to the workspace and count up,
+// the last adds them and runs the epilogue. Sums are added in K order in every
+// form, so results do not depend on timing, and no CTA waits for another outside
+// its own cluster.
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -39,8 +44,13 @@ constexpr int kGemmThreads = 192;
 constexpr int kTileM = 128;          // weight rows of a tile
 constexpr int kMaxStages = 12;
 constexpr int kGemmSmem = 227 * 1024;
+constexpr int kStaticSmem = 1024;    // the barriers
+// Two CTAs on an SM: (228 KB - 2 x 1 KB that the system takes) / 2, less the barriers.
+constexpr int kHalfSmem = 112 * 1024;
 constexpr int kMaxGrid = 160;        // CTAs the workspace has room for
 constexpr int kMaxExperts = 1024;
+constexpr int kMaxShares = 5;        // CTAs that share a grouped tile: up to 4 shares' worth, unaligned
+constexpr int kMaxCluster = 16;
 constexpr int kATile = kTileM * 128;  // bytes of a weight tile in a stage
 // Workspace: the status word at byte 0, the join counters at 1024, the partial
 // sums at 2048.
@@ -51,10 +61,14 @@ enum Source { kDense = 0, kGather = 1, kGrouped = 2 };
 
 struct GemmParams {
   int rows;      // token rows of x (dense), permuted rows (grouped)
+  int k;         // K (pair kernel, gathered rows)
+  const __nv_bfloat16* x;  // and those rows, x_stride elements apart
+  int64_t x_stride;
   int x_rows;    // rows that may be gathered
   int n;         // output features
   int kblocks;   // K in blocks of 128 bytes
-  int m_tiles, bn, stages, nbuf, tmem_cols, experts, max_split;
+  int m_tiles, bn, stages, nbuf, tmem_cols, experts;
+  int max_split;  // grouped: CTAs that may share a tile; dense: CTAs of a cluster, all on one tile
   unsigned idesc;
   const int32_t* offsets;  // [experts + 1]
   const int32_t* prow;     // source row of each permuted row
@@ -66,6 +80,7 @@ struct GemmParams {
   void* out;
   int64_t out_stride;
   int out_fp32, act;
+  int paired;  // bf16 output (and residual) whose rows allow 4-byte accesses
   unsigned* status;
   unsigned* counters;
   float* partials;
@@ -80,7 +95,18 @@ struct GemmParams {
 struct Schedule {
   int kb, grid, cta, waves, base, parts, total, a, b;
 
-  __device__ Schedule(int tiles, int kblocks, int max_split) {
+  // One tile per cluster of `split` CTAs, its K divided evenly.
+  __device__ Schedule(int kblocks, int split) {
+    kb = kblocks;
+    grid = gridDim.x;
+    cta = blockIdx.x;
+    waves = base = total = 0;
+    parts = split;
+    const int r = cta % split, t0 = cta / split * kb;
+    a = t0 + static_cast<int>(static_cast<int64_t>(r) * kb / split);
+    b = t0 + static_cast<int>(static_cast<int64_t>(r + 1) * kb / split);
+  }
+  __device__ Schedule(int tiles, int kblocks, int max_split, int) {
     kb = kblocks;
     grid = gridDim.x;
     cta = blockIdx.x;
@@ -125,6 +151,9 @@ struct Segments {  // iterates over a CTA's segments
   }
 };
 
+// Token columns that each CTA of a cluster of `split` finishes, in fours.
+__host__ __device__ constexpr int columns_each(int cols, int split) { return ((cols + split - 1) / split + 3) / 4 * 4; }
+
 struct TileAt {
   int m, expert, tok0, ntok;
 };
@@ -158,6 +187,57 @@ __device__ __forceinline__ TileAt tile_at(const GemmParams& p, const int* first,
   return t;
 }
 
+// Grouped: the first tile and first permuted row of each expert, by one warp.
+__device__ __forceinline__ void expert_tiles(const GemmParams& p, int* first, int* off, int lane) {
+  int run = 0;
+  bool bad = false;
+  for (int e0 = 0; e0 < p.experts; e0 += 32) {
+    const int e = e0 + lane;
+    int lo = 0, hi = 0;
+    if (e < p.experts) {
+      lo = __ldcg(p.offsets + e);
+      hi = __ldcg(p.offsets + e + 1);
+      bad |= lo < 0 || hi < lo || hi > p.rows;
+      lo = min(max(lo, 0), p.rows);
+      hi = min(max(hi, lo), p.rows);
+    }
+    const int t = (hi - lo + p.bn - 1) / p.bn * p.m_tiles;
+    int scan = t;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(kFull, scan, d);
+      if (lane >= d) scan += o;
+    }
+    if (e < p.experts) {
+      first[e] = run + scan - t;
+      off[e] = lo;
+      if (e == p.experts - 1) off[p.experts] = hi;
+    }
+    run += __shfl_sync(kFull, scan, 31);
+  }
+  if (lane == 0) first[p.experts] = run;
+  if (__any_sync(kFull, bad)) {  // offsets out of range: nothing is computed
+    if (lane == 0) record_error(p.status, MHC_ERR_DEVICE_INDEX);
+    __syncwarp();
+    for (int e = lane; e <= p.experts; e += 32) first[e] = 0;
+  }
+}
+
+__host__ __device__ constexpr int round32(int v) { return (v + 31) / 32 * 32; }
+
+// tile_at with an expert's rows in nearly equal tiles (multiples of 32 but the last).
+template <int SRC>
+__device__ __forceinline__ TileAt tile_even(const GemmParams& p, const int* first, const int* off, int tile) {
+  TileAt t = tile_at<SRC>(p, first, off, tile);
+  if constexpr (SRC != kDense) {
+    const int begin = off[t.expert], n = off[t.expert + 1] - begin;
+    const int tt = (n + p.bn - 1) / p.bn, each = round32((n + tt - 1) / tt);
+    t.tok0 = begin + (t.tok0 - begin) / p.bn * each;
+    t.ntok = min(each, off[t.expert + 1] - t.tok0);
+  }
+  return t;
+}
+
 // A bounded mbarrier wait: false (and the status recorded) once the budget is
 // used up; the roles then leave their loops.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, unsigned parity, const GemmParams& p) {
@@ -165,6 +245,18 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, unsigned parity, const G
   if (mbar_wait_bounded(bar, parity, wait_deadline(p.budget_ns))) return true;
   record_error(p.status, MHC_ERR_DEVICE_TIMEOUT);
   return false;
+}
+
+// A bounded wait on a barrier that other CTAs of the cluster arrive on.
+__device__ __forceinline__ bool wait_for_cluster(uint64_t* bar, unsigned parity, const GemmParams& p) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  const long long deadline = wait_deadline(p.budget_ns);
+  while (!mbar_try_wait_cluster(bar, parity))
+    if (clock64() > deadline) {
+      record_error(p.status, MHC_ERR_DEVICE_TIMEOUT);
+      return false;
+    }
+  return true;
 }
 
 __device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
@@ -181,53 +273,127 @@ __device__ __forceinline__ bool epilogue_all(bool ok) {
   return r != 0;
 }
 
+// Every thread of the cluster: what was written before its arrival is seen after
+// the wait. Whole warps.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ unsigned cluster_address(unsigned addr, int rank) {
+  unsigned r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+// 16 bytes into the shared memory of a CTA of the cluster, counted on its barrier.
+__device__ __forceinline__ void st_async4(unsigned addr, const float* v, unsigned bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1,%2,%3,%4}, [%5];" ::"r"(addr),
+               "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "r"(bar)
+               : "memory");
+}
 __device__ __forceinline__ float silu(float v) { return v / (1.f + __expf(-v)); }
 
-__device__ __forceinline__ float activate(float v, int act) {
-  switch (act) {
-    case MHC_ACT_RELU: return v > 0.f ? v : (v == v ? 0.f : v);
-    case MHC_ACT_SILU: return silu(v);
-    case MHC_ACT_GELU: return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
-    default: return v;
+// C token columns of a warp's 32 output features (thread: feature f), from the
+// sums: bias, activation, residual, one rounding, stores. Whole warps.
+template <bool GATED, int C>
+__device__ __forceinline__ void store_columns(const GemmParams& p, float (&v)[C], float (&u)[C], float bg, float bu,
+                                              int64_t tok, int f, int ntok) {
+#pragma unroll
+  for (int i = 0; i < C; ++i) v[i] += bg;
+  if constexpr (GATED) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] = silu(v[i]) * (u[i] + bu);
+  } else if (p.act == MHC_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] = silu(v[i]);
+  } else if (p.act == MHC_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] = 0.5f * v[i] * (1.f + erff(v[i] * 0.70710678118654752f));
+  } else if (p.act == MHC_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];  // NaN stays
+  }
+  const int odd = f & 1;
+  if (p.paired) {
+    // neighbouring features exchange a value, so that a thread holds two features of
+    // every other token: 4-byte accesses, half as many
+    f &= ~1;
+    const int64_t at = (tok + odd) * p.out_stride + f;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + at;
+    float2 y[C / 2];
+#pragma unroll
+    for (int i = 0; i < C / 2; ++i) {
+      const float got = __shfl_xor_sync(kFull, odd ? v[2 * i] : v[2 * i + 1], 1);
+      y[i] = odd ? make_float2(got, v[2 * i + 1]) : make_float2(v[2 * i], got);
+    }
+    const int n = f < p.n ? ntok - odd : 0;  // this thread's tokens: 0, 2, 4, ... below n
+    if (p.residual != nullptr) {
+      const __nv_bfloat16* res = p.residual + (tok + odd) * p.res_stride + f;
+      unsigned r[C / 2];
+#pragma unroll
+      for (int i = 0; i < C / 2; ++i)
+        r[i] = 2 * i < n ? *reinterpret_cast<const unsigned*>(res + 2 * i * p.res_stride) : 0u;
+#pragma unroll
+      for (int i = 0; i < C / 2; ++i) {
+        y[i].x += __uint_as_float(r[i] << 16);
+        y[i].y += __uint_as_float(r[i] & 0xffff0000u);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < C / 2; ++i)
+      // fp32 sums throughout; a bf16 output is rounded here, once
+      if (2 * i < n) *reinterpret_cast<unsigned*>(dst + 2 * i * p.out_stride) = pack_bf16x2(y[i].x, y[i].y);
+    return;
+  }
+  if (f >= p.n) return;
+  if (p.residual != nullptr) {
+    const __nv_bfloat16* res = p.residual + tok * p.res_stride + f;
+    float r[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) r[i] = i < ntok ? __bfloat162float(res[i * p.res_stride]) : 0.f;
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] += r[i];
+  }
+  const int64_t at = tok * p.out_stride + f;
+  if (p.out_fp32) {
+    float* dst = static_cast<float*>(p.out) + at;
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+      if (i < ntok) dst[i * p.out_stride] = v[i];
+  } else {
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + at;
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+      if (i < ntok) dst[i * p.out_stride] = __float2bfloat16(v[i]);
   }
 }
 
-// 16 token columns of a thread's output feature: activation, residual, store.
+// 16 columns of a thread's feature.
 template <bool GATED>
-__device__ __forceinline__ void store16(const GemmParams& p, float (&v)[16], float (&u)[16], float bg, float bu,
-                                        int64_t tok, int f, int ntok) {
-  float res[16];
-  if (p.residual != nullptr) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      res[i] = i < ntok ? __bfloat162float(p.residual[(tok + i) * p.res_stride + f]) : 0.f;
-  }
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    float y = v[i] + bg;
-    y = GATED ? silu(y) * (u[i] + bu) : activate(y, p.act);
-    if (p.residual != nullptr) y += res[i];
-    if (i < ntok) {
-      const int64_t at = (tok + i) * p.out_stride + f;
-      // fp32 sums throughout; a bf16 output is rounded here, once
-      if (p.out_fp32) static_cast<float*>(p.out)[at] = y;
-      else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16(y);
-    }
-  }
+__device__ __forceinline__ void read_sums(unsigned src, int bn, float (&v)[16], float (&u)[16]) {
+  tmem_ld16(src, v);
+  if constexpr (GATED) tmem_ld16(src + bn, u);
+  tmem_ld_wait();
+}
+
+__device__ __forceinline__ void add4(float (&v)[4], const float4 a) {
+  v[0] += a.x;
+  v[1] += a.y;
+  v[2] += a.z;
+  v[3] += a.w;
 }
 
 // ---------------------------------------------------------------- kernel
 
-template <bool FP8, bool GATED, int SRC>
-__global__ void __launch_bounds__(kGemmThreads, 1)
+template <bool FP8, bool GATED, int SRC, int CTAS>
+__global__ void __launch_bounds__(kGemmThreads, CTAS)
     gemm_kernel(const __grid_constant__ GemmParams p, const __grid_constant__ CUtensorMap tm_w,
                 const __grid_constant__ CUtensorMap tm_x) {
   extern __shared__ unsigned char raw[];
-  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
+  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], sums_in;
   __shared__ unsigned tmem_slot, join_slot;
+  __shared__ __align__(16) int rows[SRC == kGather ? 128 : 4];  // gathered token rows of the tile being copied
   constexpr int kAcc = GATED ? 2 : 1;
   constexpr int kElems = FP8 ? 128 : 64;  // K elements of a stage's 128-byte rows
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(kFull, tid >> 5, 0);  // uniform
   const int x_bytes = p.bn * 128;
   const int sf_bytes = FP8 ? (kAcc + 1) * 512 : 0;
   const unsigned smem0 = (smem_u32(raw) + 1023u) & ~1023u;
@@ -235,6 +401,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   // bn is a multiple of 16 rows, so a stage's token rows start on the 1024-byte
   // boundary that the swizzle pattern repeats at
   const unsigned sf0 = x0 + p.stages * x_bytes;
+  // a cluster's sums of this CTA's columns: [CTA][gate, up][column / 4][feature][4]
+  const unsigned sums0 = sf0 + p.stages * sf_bytes;
   int* first = nullptr;  // grouped: first tile of each expert, and its first permuted row
   int* off = nullptr;
   if constexpr (SRC != kDense) {
@@ -253,6 +421,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], 128);
     }
+    mbar_init(&sums_in, 1);
   }
   if (warp == 1) {
     tmem_alloc(&tmem_slot, p.tmem_cols);
@@ -262,54 +431,37 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   if constexpr (SRC == kDense) {
     tiles = p.m_tiles * ((p.rows + p.bn - 1) / p.bn);
   } else {
-    griddep_wait();  // the offsets are the preceding kernel's
-    if (warp == 0) {
-      int run = 0;
-      bool bad = false;
-      for (int e0 = 0; e0 < p.experts; e0 += 32) {
-        const int e = e0 + lane;
-        int lo = 0, hi = 0;
-        if (e < p.experts) {
-          lo = p.offsets[e];
-          hi = p.offsets[e + 1];
-          bad |= lo < 0 || hi < lo || hi > p.rows;
-          lo = min(max(lo, 0), p.rows);
-          hi = min(max(hi, lo), p.rows);
-        }
-        int t = (hi - lo + p.bn - 1) / p.bn * p.m_tiles;
-        int scan = t;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int o = __shfl_up_sync(kFull, scan, d);
-          if (lane >= d) scan += o;
-        }
-        if (e < p.experts) {
-          first[e] = run + scan - t;
-          off[e] = lo;
-          if (e == p.experts - 1) off[p.experts] = hi;
-        }
-        run += __shfl_sync(kFull, scan, 31);
-      }
-      if (lane == 0) first[p.experts] = run;
-      if (__any_sync(kFull, bad)) {  // offsets out of range: nothing is computed
-        if (lane == 0) record_error(p.status, MHC_ERR_DEVICE_INDEX);
-        __syncwarp();
-        for (int e = lane; e <= p.experts; e += 32) first[e] = 0;
-      }
-    }
+    // The offsets are the preceding kernel's. The second product's preceding kernel is
+    // the first, which let it start only after it had itself waited for the offsets:
+    // they are there (and read from L2), and the second product can ask for its
+    // weights while the first ends.
+    if constexpr (SRC == kGather) griddep_wait();
+    if (warp == 0) expert_tiles(p, first, off, lane);
   }
   tcgen05_fence_before();
   __syncthreads();
   tcgen05_fence_after();
+  const bool clustered = SRC == kDense && p.max_split > 1;
+  if (clustered) {
+    if (tid == 0) {  // the sums that the cluster will send for this CTA's columns
+      const TileAt t = tile_at<SRC>(p, first, off, blockIdx.x / p.max_split);
+      const int r = blockIdx.x % p.max_split, each = columns_each(t.ntok, p.max_split);
+      const int fours = (min(each, max(0, t.ntok - r * each)) + 3) / 4;
+      mbar_arrive_expect_tx(&sums_in, static_cast<unsigned>(fours) * 4 * kAcc * p.max_split * kTileM * 4);
+    }
+    __syncwarp();
+    cluster_arrive();  // this CTA runs and its barriers are set
+  }
+  griddep_launch_dependents();
   if constexpr (SRC != kDense) tiles = first[p.experts];
   const unsigned tmem = tmem_slot;
-  const Schedule sched(tiles, p.kblocks, p.max_split);
-  const int acc_cols = kAcc * p.bn;
+  const Schedule sched = clustered ? Schedule(p.kblocks, p.max_split) : Schedule(tiles, p.kblocks, p.max_split, 0);
+  const int acc_cols = kAcc * p.bn;  // of one tile
 
   if (warp == 0) {
     // ------------------------------------------------ copies
     const unsigned stage_bytes = kAcc * kATile + x_bytes + sf_bytes;
-    auto load_w = [&](int s, const TileAt& t, int kb) {  // lane 0
+    auto load_w = [&](int s, const TileAt& t, int kb) {  // one lane
       mbar_arrive_expect_tx(&full[s], stage_bytes + p.extra_tx);
       const int row = (SRC == kDense ? 0 : t.expert * (kAcc * p.n)) + t.m * kTileM;
       const unsigned dst = smem0 + s * (kAcc * kATile);
@@ -324,18 +476,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       }
     };
     int ahead = 0;  // stages whose weights were requested before the wait
-    if constexpr (SRC == kDense) {
+    if constexpr (SRC != kGather) {
       // The weights are not the preceding kernel's to write: the first stages'
       // are requested before waiting for it.
-      if (lane == 0) {
-        Segments it(sched);
-        Segment g;
-        while (ahead < p.stages && it.next(g)) {
-          const TileAt t = tile_at<SRC>(p, first, off, g.tile);
-          for (int kb = g.k0; kb < g.k1 && ahead < p.stages; ++kb) load_w(ahead++, t, kb);
-        }
+      Segments it(sched);
+      Segment g;
+      while (ahead < p.stages && it.next(g)) {
+        const TileAt t = tile_at<SRC>(p, first, off, g.tile);
+        for (int kb = g.k0; kb < g.k1 && ahead < p.stages; ++kb, ++ahead)
+          if (elect_one()) load_w(ahead, t, kb);
       }
-      ahead = __shfl_sync(kFull, ahead, 0);
+      __syncwarp();
       griddep_wait();
     }
     Segments it(sched);
@@ -345,24 +496,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     bool ok = true;
     while (ok && it.next(g)) {
       const TileAt t = tile_at<SRC>(p, first, off, g.tile);
-      int4 idx = make_int4(0, 0, 0, 0);
       if constexpr (SRC == kGather) {
-        // lane l gathers rows 4l..4l+3 of the tile; what lies behind the last
-        // row, or names no row of x, reads row 0 and is not stored, or is
-        // recorded as an error
-        int r[4];
-        bool bad = false;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int c = 4 * lane + q;
-          r[q] = c < t.ntok ? p.prow[t.tok0 + c] : 0;
-          if (r[q] < 0 || r[q] >= p.x_rows) {
-            bad = true;
-            r[q] = 0;
+        // the tile's token rows; what lies behind the last row, or names no row of
+        // x, reads row 0 and is not stored, or is recorded as an error
+        __syncwarp();
+        for (int c = lane; c < p.bn; c += 32) {
+          int r = c < t.ntok ? p.prow[t.tok0 + c] : 0;
+          if (r < 0 || r >= p.x_rows) {
+            record_error(p.status, MHC_ERR_DEVICE_INDEX);
+            r = 0;
           }
+          rows[c] = r;
         }
-        if (bad) record_error(p.status, MHC_ERR_DEVICE_INDEX);
-        idx = make_int4(r[0], r[1], r[2], r[3]);
+        __syncwarp();
       }
       for (int kb = g.k0; kb < g.k1; ++kb, ++i) {
         if (i >= ahead) {
@@ -371,25 +517,27 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             ok = false;
             break;
           }
-          if (lane == 0) load_w(s, t, kb);
+          if (elect_one()) load_w(s, t, kb);
           __syncwarp();
         }
         const unsigned dst = x0 + s * x_bytes;
         if constexpr (SRC == kGather) {
-          if (lane < p.bn / 4) tma_gather4(dst + lane * 512, &tm_x, kb * kElems, idx, &full[s]);
-        } else if (lane == 0) {
+          if (elect_one())
+            for (int j = 0; j < p.bn / 4; ++j)
+              tma_gather4(dst + j * 512, &tm_x, kb * kElems, reinterpret_cast<const int4*>(rows)[j], &full[s]);
+        } else if (elect_one()) {
           tma_load_2d(dst, &tm_x, kb * kElems, t.tok0, &full[s]);
           if constexpr (FP8)
             bulk_g2s(raw + (sf0 - smem_u32(raw)) + s * sf_bytes + kAcc * 512,
                      p.x_scale + (static_cast<size_t>(t.tok0 / 128) * p.kblocks + kb) * 512, 512, &full[s]);
         }
+        __syncwarp();
         if (++s == p.stages) {
           s = 0;
           ph ^= 1;
         }
       }
     }
-    griddep_launch_dependents();
     if (!ok) {  // leave no copy in flight behind: wait (bounded) for the requested stages
       const long long deadline = wait_deadline(p.budget_ns);
       for (int q = 0; q < p.stages && q < i; ++q) {
@@ -397,22 +545,28 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         mbar_wait_bounded(&full[q], n & 1u, deadline);
       }
     }
+    if (clustered) {
+      __syncwarp();
+      cluster_wait();
+      cluster_arrive();
+    }
   } else if (warp == 1) {
     // ------------------------------------------------ products
-    if (lane == 0) {
-      Segments it(sched);
-      Segment g;
-      int s = 0, buf = 0;
-      unsigned ph = 0, aph = 1;
-      bool ok = true;
-      while (ok && it.next(g)) {
-        if (!(ok = wait_for(&acc_empty[buf], aph, p))) break;
+    const unsigned a_lo = desc_lo(smem0), b_lo = desc_lo(x0), idesc = p.idesc;
+    Segments it(sched);
+    Segment g;
+    int s = 0, buf = 0;
+    unsigned ph = 0, aph = 1;
+    bool ok = true;
+    while (ok && it.next(g)) {
+      if (!(ok = __all_sync(kFull, wait_for(&acc_empty[buf], aph, p)))) break;
+      tcgen05_fence_after();
+      const unsigned d = tmem + buf * acc_cols;
+      for (int kb = g.k0; kb < g.k1; ++kb) {
+        if (!(ok = __all_sync(kFull, wait_for(&full[s], ph, p)))) break;
         tcgen05_fence_after();
-        const unsigned d = tmem + buf * acc_cols;
-        for (int kb = g.k0; kb < g.k1; ++kb) {
-          if (!(ok = wait_for(&full[s], ph, p))) break;
-          tcgen05_fence_after();
-          const unsigned a = smem0 + s * (kAcc * kATile), b = x0 + s * x_bytes;
+        if (elect_one()) {
+          const unsigned a = a_lo + s * (kAcc * kATile / 16), b = b_lo + s * (x_bytes / 16);
           unsigned sf = 0;
           if constexpr (FP8) {
             // one set of scale columns per stage: a set is rewritten only after
@@ -423,46 +577,50 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             for (int q = 0; q <= kAcc; ++q) tmem_copy_scales(sf + 4 * q, desc_scales(src + 512 * q));
           }
 #pragma unroll
-          for (int q = 0; q < kAcc; ++q) {
+          for (int k = 0; k < 4; ++k)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint64_t da = desc_sw128(a + q * kATile) + 2 * k, db = desc_sw128(b) + 2 * k;
-              const bool accumulate = kb > g.k0 || k > 0;
+            for (int q = 0; q < kAcc; ++q) {
+              const unsigned da = a + q * (kATile / 16) + 2 * k;
               if constexpr (FP8)
-                mma_mxf8(d + q * p.bn, da, db, p.idesc | (k << 4) | (k << 29), sf + 4 * q, sf + 4 * kAcc, accumulate);
+                mma_mxf8(d + q * p.bn, da, b + 2 * k, idesc | (k << 4) | (k << 29), sf + 4 * q, sf + 4 * kAcc,
+                         k > 0 || kb > g.k0);
               else
-                mma_bf16(d + q * p.bn, da, db, p.idesc, accumulate);
+                mma_bf16(d + q * p.bn, da, b + 2 * k, idesc, k > 0 || kb > g.k0);
             }
-          }
           mma_commit(&empty[s]);
-          if (++s == p.stages) {
-            s = 0;
-            ph ^= 1;
-          }
+          if (kb == g.k1 - 1) mma_commit(&acc_full[buf]);
         }
-        if (!ok) break;
-        mma_commit(&acc_full[buf]);
-        if (++buf == p.nbuf) {
-          buf = 0;
-          aph ^= 1;
+        __syncwarp();
+        if (++s == p.stages) {
+          s = 0;
+          ph ^= 1;
         }
+      }
+      if (!ok) break;
+      if (++buf == p.nbuf) {
+        buf = 0;
+        aph ^= 1;
       }
     }
     __syncwarp();
+    if (clustered) {
+      cluster_wait();
+      cluster_arrive();
+    }
   } else {
     // ------------------------------------------------ epilogue
-    if constexpr (SRC == kDense) griddep_wait();
+    if constexpr (SRC != kGather) griddep_wait();
     const int q = warp & 3;  // the quarter of the accumulator's lanes this warp can read
     Segments it(sched);
     Segment g;
     int buf = 0;
     unsigned ph = 0;
+    bool sent = false;
     while (it.next(g)) {
       const TileAt t = tile_at<SRC>(p, first, off, g.tile);
       const int f = t.m * kTileM + q * 32 + lane;
-      const bool mine = f < p.n;
       float bg = 0.f, bu = 0.f;
-      if (p.bias != nullptr && mine) {
+      if (p.bias != nullptr && f < p.n) {
         bg = p.bias[f];
         if constexpr (GATED) bu = p.bias[p.n + f];
       }
@@ -470,15 +628,41 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       tcgen05_fence_after();
       const unsigned src = tmem + buf * acc_cols + (static_cast<unsigned>(q * 32) << 16);
       const bool whole = g.k0 == 0 && g.k1 == p.kblocks;
-      const size_t slot_floats = static_cast<size_t>(acc_cols) * kTileM;
+      const size_t slot_floats = static_cast<size_t>(kAcc) * p.bn * kTileM;
+      if (clustered) {
+        // token column c is finished by CTA c / each of the cluster; a thread sends four
+        // columns at a time (columns behind the last are sent and not used)
+        const int S = p.max_split, each = columns_each(t.ntok, S);
+        const unsigned mine_at = sums0 + (sched.cta % S) * (kAcc * each * kTileM * 4) + (q * 32 + lane) * 16;
+        cluster_wait();
+        int owner = 0, at = 0;
+        unsigned dst = cluster_address(mine_at, 0), bar = cluster_address(smem_u32(&sums_in), 0);
+        for (int c = 0; c < t.ntok; c += 16) {
+          float v[16], u[16];
+          read_sums<GATED>(src + c, p.bn, v, u);
+#pragma unroll
+          for (int i = 0; i < 16; i += 4)
+            if (c + i < t.ntok) {
+              st_async4(dst + at * (kTileM * 4), v + i, bar);
+              if constexpr (GATED) st_async4(dst + (each + at) * (kTileM * 4), u + i, bar);
+              if ((at += 4) == each) {
+                at = 0;
+                owner = min(owner + 1, S - 1);
+                dst = cluster_address(mine_at, owner);
+                bar = cluster_address(smem_u32(&sums_in), owner);
+              }
+            }
+        }
+        sent = true;
+        break;
+      }
+      // partial sums of a shared tile in the workspace, [column][feature]
       float* slot = p.partials + (static_cast<size_t>(sched.cta) * 2 + (g.k0 > 0 ? 0 : 1)) * slot_floats + q * 32 + lane;
       for (int c = 0; c < t.ntok; c += 16) {
         float v[16], u[16];
-        tmem_ld16(src + c, v);
-        if constexpr (GATED) tmem_ld16(src + p.bn + c, u);
-        tmem_ld_wait();
+        read_sums<GATED>(src + c, p.bn, v, u);
         if (whole) {
-          if (mine) store16<GATED>(p, v, u, bg, bu, t.tok0 + c, f, t.ntok - c);
+          store_columns<GATED, 16>(p, v, u, bg, bu, t.tok0 + c, f, t.ntok - c);
         } else {
 #pragma unroll
           for (int i = 0; i < 16; ++i)
@@ -495,36 +679,79 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         ph ^= 1;
       }
       if (whole) continue;
-      // the tile is shared: the CTA that counts last joins the sums
-      const int w0 = (g.tile - sched.base) * p.kblocks;
-      const int c0 = sched.owner(w0), c1 = sched.owner(w0 + p.kblocks - 1);
-      __threadfence();
-      epilogue_barrier();
-      if (warp == 2 && lane == 0) join_slot = atomicAdd(&p.counters[c0], 1u);
-      epilogue_barrier();
-      const bool last = join_slot == static_cast<unsigned>(c1 - c0);
-      epilogue_barrier();  // join_slot is rewritten by the next shared tile
-      if (!last) continue;
-      __threadfence();
-      if (warp == 2 && lane == 0) p.counters[c0] = 0;  // for the next launch
-      for (int c = 0; c < t.ntok; c += 16) {
-        float v[16], u[16];
+      if constexpr (SRC != kDense) {
+        // the tile is shared: the CTA that counts last joins the sums
+        const int w0 = (g.tile - sched.base) * p.kblocks;
+        const int c0 = sched.owner(w0), c1 = sched.owner(w0 + p.kblocks - 1);
+        __threadfence();
+        epilogue_barrier();
+        if (warp == 2 && lane == 0) join_slot = atomicAdd(&p.counters[c0], 1u);
+        epilogue_barrier();
+        const bool last = join_slot == static_cast<unsigned>(c1 - c0);
+        epilogue_barrier();  // join_slot is rewritten by the next shared tile
+        if (!last) continue;
+        __threadfence();
+        if (warp == 2 && lane == 0) p.counters[c0] = 0;  // for the next launch
+        const float* from[kMaxShares];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = u[i] = 0.f;
-        for (int k = c0; k <= c1; ++k) {
-          const float* from = p.partials +
-                              (static_cast<size_t>(k) * 2 + (sched.start_of(k) > w0 ? 0 : 1)) * slot_floats + q * 32 +
-                              lane;
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (c + i < t.ntok) {
-              v[i] += __ldcg(from + (c + i) * kTileM);
-              if constexpr (GATED) u[i] += __ldcg(from + (p.bn + c + i) * kTileM);
-            }
+        for (int k = 0; k < kMaxShares; ++k) {
+          const int o = min(c0 + k, c1);
+          from[k] = p.partials + (static_cast<size_t>(o) * 2 + (sched.start_of(o) > w0 ? 0 : 1)) * slot_floats + q * 32 +
+                    lane;
         }
-        if (mine) store16<GATED>(p, v, u, bg, bu, t.tok0 + c, f, t.ntok - c);
+        const int shares = c1 - c0 + 1;
+        for (int c = 0; c < t.ntok; c += 4) {
+          float v[kMaxShares][4], u[kMaxShares][4];
+#pragma unroll
+          for (int k = 0; k < kMaxShares; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const bool has = k < shares && c + i < t.ntok;
+              v[k][i] = has ? __ldcg(from[k] + (c + i) * kTileM) : 0.f;
+              if constexpr (GATED) u[k][i] = has ? __ldcg(from[k] + (p.bn + c + i) * kTileM) : 0.f;
+            }
+#pragma unroll
+          for (int k = 1; k < kMaxShares; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              v[0][i] += v[k][i];
+              if constexpr (GATED) u[0][i] += u[k][i];
+            }
+          store_columns<GATED, 4>(p, v[0], u[0], bg, bu, t.tok0 + c, f, t.ntok - c);
+        }
       }
     }
+    if (clustered) {
+      __syncwarp();
+      if (!sent) cluster_wait();
+      cluster_arrive();
+      const bool in = sent && wait_for_cluster(&sums_in, 0, p);
+      if (in) {
+        const int S = p.max_split, r = sched.cta % S;
+        const TileAt t = tile_at<SRC>(p, first, off, sched.cta / S);
+        const int row = q * 32 + lane, f = t.m * kTileM + row;
+        float bg = 0.f, bu = 0.f;
+        if (p.bias != nullptr && f < p.n) {
+          bg = p.bias[f];
+          if constexpr (GATED) bu = p.bias[p.n + f];
+        }
+        const int each = columns_each(t.ntok, S), n = min(each, t.ntok - r * each);
+        const float4* from = reinterpret_cast<const float4*>(raw + (sums0 - smem_u32(raw))) + row;
+        for (int c = 0; c < n; c += 4) {
+          float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+          for (int k = 0; k < S; ++k) {
+            add4(v, from[(k * kAcc * each + c) / 4 * kTileM]);
+            if constexpr (GATED) add4(u, from[((k * kAcc + 1) * each + c) / 4 * kTileM]);
+          }
+          store_columns<GATED, 4>(p, v, u, bg, bu, t.tok0 + r * each + c, f, n - c);
+        }
+      }
+    }
+  }
+  if (clustered) {
+    __syncwarp();
+    cluster_wait();  // no CTA leaves while another may still send to it
   }
   tcgen05_fence_before();
   __syncthreads();
@@ -535,6 +762,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 }
 
 }  // namespace mhc
+
+#include "mhc_pair.cuh"
 
 // =====================================================================================
 // Host side
@@ -547,12 +776,10 @@ using namespace mhc;
 constexpr int kMaxTokens = 65535;
 constexpr int kMaxK = 65536;
 constexpr int kMaxFeatures = 1 << 20;
-constexpr int kMaxSplit = 16;
+constexpr int kSplitCols = 32;  // most token columns of a tile that several CTAs may share
 
-size_t partial_bytes(int rows) {
-  const int cols = rows >= 128 ? 256 : 2 * ((rows + 15) / 16 * 16);
-  return static_cast<size_t>(kMaxGrid) * 2 * kTileM * cols * 4;
-}
+// Partial sums of the experts' shared tiles: two per CTA, gate and up.
+constexpr size_t kPartialBytes = static_cast<size_t>(kMaxGrid) * 2 * kTileM * 2 * kSplitCols * 4;
 
 // A row-major matrix as a 2-D map: rows of `cols` elements, `stride` bytes apart;
 // boxes of 128 bytes x box_rows in the 128-byte swizzle. What lies outside reads
@@ -568,48 +795,57 @@ bool make_map2(CUtensorMap* m, const void* base, bool bytes, uint64_t cols, uint
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Shared memory of the sums that a cluster's CTAs send one of them.
+int sums_bytes(int bn, int acc, int split) { return columns_each(bn, split) * split * acc * kTileM * 4; }
+
 // bn, kblocks and the operand types are set: the ring, tensor memory and
 // instruction descriptor that go with them, and the launch.
-template <bool FP8, bool GATED, int SRC>
-mhc_status launch_gemm(GemmParams& p, const CUtensorMap& w, const CUtensorMap& x, int grid, cudaStream_t stream) {
+template <bool FP8, bool GATED, int SRC, int CTAS>
+mhc_status launch_gemm(GemmParams& p, const CUtensorMap& w, const CUtensorMap& x, int grid, int cluster,
+                       cudaStream_t stream) {
   constexpr int acc = GATED ? 2 : 1;
   const int fixed = 1024 + (SRC == kDense ? 0 : 8 * (p.experts + 1));
   const int stage = acc * kATile + p.bn * 128 + (FP8 ? (acc + 1) * 512 : 0);
-  const int static_smem = 1024;  // the barriers
-  p.stages = (kGemmSmem - static_smem - fixed) / stage;
+  const int limit = CTAS == 2 ? kHalfSmem : kGemmSmem - kStaticSmem;
+  const int sums = cluster > 1 ? sums_bytes(p.bn, acc, cluster) : 0;
+  p.stages = (limit - fixed - sums) / stage;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
-  const int smem = fixed + p.stages * stage;
+  const int smem = fixed + p.stages * stage + sums;
   auto cols = [&](int nbuf) { return nbuf * acc * p.bn + (FP8 ? p.stages * (acc + 1) * 4 : 0); };
-  p.nbuf = cols(2) <= 512 ? 2 : 1;
+  p.nbuf = cluster == 1 && cols(2) <= 512 / CTAS ? 2 : 1;
   p.tmem_cols = 32;
   while (p.tmem_cols < cols(p.nbuf)) p.tmem_cols *= 2;
-  if (p.stages < 2 || p.tmem_cols > 512) return MHC_ERR_UNSUPPORTED_SHAPE;
+  if (p.stages < 2 || p.tmem_cols > 512 / CTAS) return MHC_ERR_UNSUPPORTED_SHAPE;
   p.idesc = (static_cast<unsigned>(p.bn >> 3) << 17) | (static_cast<unsigned>(kTileM >> 4) << 24) |
             (FP8 ? (1u << 23) : (1u << 4) | (1u << 7) | (1u << 10));
   p.budget_ns = g_budget_ns;
   p.extra_tx = static_cast<unsigned>(g_extra_tx) * 16;
-  auto kern = gemm_kernel<FP8, GATED, SRC>;
+  auto kern = gemm_kernel<FP8, GATED, SRC, CTAS>;
   static std::atomic<int> configured[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MHC_ERR_CUDA;
   if (configured[dev].load(std::memory_order_acquire) == 0) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem - static_smem) !=
-        cudaSuccess) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem - kStaticSmem) !=
+            cudaSuccess ||
+        (SRC == kDense && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)) {
       (void)cudaGetLastError();
       return MHC_ERR_CUDA;
     }
     configured[dev].store(1, std::memory_order_release);
   }
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kGemmThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   if (cudaLaunchKernelEx(&cfg, kern, p, w, x) != cudaSuccess) {
     (void)cudaGetLastError();
     return MHC_ERR_CUDA;
@@ -624,13 +860,125 @@ int gemm_grid() {
 
 int round16(int v) { return (v + 15) / 16 * 16; }
 
+struct Plan {
+  int bn, split, per_sm, grid;
+};
+
+// CTAs that are resident at once in clusters of 1..16, at one and two CTAs an SM,
+// as cudaOccupancyMaxActiveClusters counts them on a B200 (148 SMs in clusters of
+// SMs that larger clusters do not fill).
+constexpr int kRoom[2][16] = {{148, 148, 135, 132, 130, 132, 105, 120, 108, 110, 99, 84, 91, 98, 105, 112},
+                              {296, 296, 279, 284, 280, 270, 259, 264, 243, 260, 253, 252, 234, 224, 210, 224}};
+
+// Token columns of a tile and CTAs per tile of a dense product: the least of a
+// simple estimate of the time, in SM cycles. A K block costs the larger of its
+// products (128 x bn x 64 bf16 multiply-adds at 4096 a cycle) and its copies (what
+// the ring holds, once per memory latency, at most kCopyRate bytes a cycle and SM
+// and the memory's rate over all SMs); a tile adds its epilogue.
+Plan plan_linear(const GemmParams& p, int rows, bool fp8, bool gated) {
+  constexpr double kCopyRate = 60, kLatency = 2400, kMemoryRate = 3500, kTileCost = 2500;
+  const int sms = gemm_grid();
+  const int acc = gated ? 2 : 1;
+  const int cap = fp8 || gated ? 128 : 256;
+  Plan best{0, 1, 1, 1};
+  double least = 0;
+  for (int bn = round16(rows < cap ? rows : cap); bn >= 16; bn -= 16) {
+    if (fp8 && rows > bn && bn != 128) continue;  // a token tile starts at a scale tile's first row
+    const int tiles = p.m_tiles * ((rows + bn - 1) / bn);
+    const int stage = acc * kATile + bn * 128 + (fp8 ? (acc + 1) * 512 : 0);
+    const int cols = acc * bn + (fp8 ? kMaxStages * (acc + 1) * 4 : 0);
+    for (int per_sm = 1; per_sm <= 2; ++per_sm) {
+      for (int split = 1; split <= kMaxCluster && split <= p.kblocks; ++split) {
+        if (split > 1 && tiles * split > kRoom[per_sm - 1][split - 1]) continue;
+        const int room = (per_sm == 2 ? kHalfSmem : kGemmSmem - kStaticSmem) - 1024 -
+                         (split > 1 ? sums_bytes(bn, acc, split) : 0);
+        int stages = room / stage < kMaxStages ? room / stage : kMaxStages;
+        if (stages < 2 || cols > 512 / per_sm) continue;
+        const int ctas = split > 1 ? tiles * split : (tiles < sms ? tiles : sms);
+        const int waves = split > 1 ? 1 : (tiles + sms - 1) / sms;
+        const int blocks = (p.kblocks + split - 1) / split;
+        if (stages > blocks) stages = blocks;
+        const double shared = ctas > sms ? static_cast<double>(ctas) / sms : 1.0;  // CTAs on one SM
+        const double bytes = acc * kATile + bn * 128;
+        double rate = stages * bytes / kLatency;
+        if (rate > kCopyRate / shared) rate = kCopyRate / shared;
+        if (rate > kMemoryRate / ctas) rate = kMemoryRate / ctas;
+        const double products = 2.0 * acc * bn * shared;
+        const double block = products > bytes / rate ? products : bytes / rate;
+        // a cluster's epilogue: its sums sent, and its columns finished
+        const double join = split > 1 ? 600 + 12.0 * acc * bn + 60.0 * columns_each(bn, split) : 24.0 * acc * bn;
+        const double t = waves * blocks * block + kTileCost + join;
+        if (best.bn == 0 || t < least) {
+          least = t;
+          best = Plan{bn, split, split > 1 ? per_sm : 1, ctas};
+        }
+      }
+    }
+  }
+  return best;
+}
+
+// Whether the pair kernel takes a product: enough token rows to be bound by the
+// tensor cores or L2 rather than by reading the weights once.
+constexpr int kPairRows = 192;   // of a dense product
+constexpr int kPairMean = 96;    // of an expert, on average
+
+template <bool GATED, int SRC>
+mhc_status launch_pair(GemmParams& p, const CUtensorMap& w, const CUtensorMap& x, cudaStream_t stream) {
+  constexpr int acc = GATED ? 2 : 1;
+  const int fixed = 1024 + (SRC == kDense ? 0 : 8 * (p.experts + 1));
+  const int stage = acc * kATile + p.bn / 2 * 128;
+  p.stages = (kGemmSmem - kStaticSmem - fixed) / stage;
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  p.nbuf = 2 * acc * p.bn <= 512 ? 2 : 1;
+  if (p.stages <= kPairLag || p.bn % 32 != 0 || acc * p.bn > 512) return MHC_ERR_UNSUPPORTED_SHAPE;
+  p.m_tiles = (p.n + kPairTileM - 1) / kPairTileM;
+  p.idesc = (static_cast<unsigned>(kPairTileM >> 4) << 24) | (1u << 4) | (1u << 7) | (1u << 10);
+  p.budget_ns = g_budget_ns;
+  p.extra_tx = static_cast<unsigned>(g_extra_tx) * 16;
+  auto kern = pair_kernel<GATED, SRC>;
+  static std::atomic<int> configured[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MHC_ERR_CUDA;
+  if (configured[dev].load(std::memory_order_acquire) == 0) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem - kStaticSmem) !=
+        cudaSuccess) {
+      (void)cudaGetLastError();
+      return MHC_ERR_CUDA;
+    }
+    configured[dev].store(1, std::memory_order_release);
+  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(gemm_grid() / 2 * 2);
+  cfg.blockDim = dim3(SRC == kGather ? 320 : 192);
+  cfg.dynamicSmemBytes = fixed + p.stages * stage;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, p, w, x) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return MHC_ERR_CUDA;
+  }
+  return MHC_OK;
+}
+
+template <bool FP8, bool GATED>
+mhc_status launch_linear(GemmParams& p, const Plan& plan, const CUtensorMap& w, const CUtensorMap& x,
+                         cudaStream_t stream) {
+  return plan.per_sm == 2 ? launch_gemm<FP8, GATED, kDense, 2>(p, w, x, plan.grid, plan.split, stream)
+                          : launch_gemm<FP8, GATED, kDense, 1>(p, w, x, plan.grid, plan.split, stream);
+}
+
 }  // namespace
 
 extern "C" {
 
 size_t mhc_linear_workspace_bytes(int rows) {
   if (rows < 1 || rows > kMaxTokens) return 0;
-  return kGemmHeader + partial_bytes(rows);
+  return kGemmHeader;
 }
 
 mhc_status mhc_linear(const void* x, const uint8_t* x_scale, int64_t x_stride, const void* weight,
@@ -658,7 +1006,6 @@ mhc_status mhc_linear(const void* x, const uint8_t* x_scale, int64_t x_stride, c
   p.n = out_features;
   p.kblocks = fp8 ? (in_features + 127) / 128 : (in_features + 63) / 64;
   p.m_tiles = (out_features + kTileM - 1) / kTileM;
-  p.max_split = kMaxSplit;
   p.x_scale = x_scale;
   p.w_scale = weight_scale;
   p.bias = bias;
@@ -668,43 +1015,28 @@ mhc_status mhc_linear(const void* x, const uint8_t* x_scale, int64_t x_stride, c
   p.out_stride = out_stride;
   p.out_fp32 = out_fp32 != 0;
   p.act = activation;
+  p.paired = !out_fp32 && aligned(out, 4) && out_stride % 2 == 0 && out_features % 2 == 0 && aligned(residual, 4) &&
+             residual_stride % 2 == 0;
   p.status = static_cast<unsigned*>(workspace);
-  p.counters = reinterpret_cast<unsigned*>(static_cast<char*>(workspace) + kGemmCounters);
-  p.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + kGemmHeader);
-  // Token columns of a tile: all tokens if one tile can hold them, else tiles of
-  // 128 (MXFP8, whose scale tiles are 128 rows, and gated products, which hold
-  // two accumulators) or of nearly equal parts of up to 256.
-  const int cap = fp8 || gated ? 128 : 256;
-  if (rows <= cap) {
-    p.bn = round16(rows);
-  } else if (fp8) {
-    p.bn = 128;
-  } else {
-    const int tt = (rows + cap - 1) / cap;
-    p.bn = round16((rows + tt - 1) / tt);
-  }
-  const int tiles = p.m_tiles * ((rows + p.bn - 1) / p.bn);
-  int grid = gemm_grid();
-  if (tiles < grid) {  // as many CTAs as the schedule makes shares
-    int64_t most = static_cast<int64_t>(tiles) * kMaxSplit;
-    const int64_t pairs = static_cast<int64_t>(tiles) * p.kblocks / 2;
-    if (pairs < most) most = pairs > tiles ? pairs : tiles;
-    if (most < grid) grid = static_cast<int>(most);
-  }
+  const Plan plan = plan_linear(p, rows, fp8, gated);
+  const bool pair = !fp8 && rows > kPairRows && plan.split == 1;
+  p.bn = pair ? 256 : plan.bn;
+  p.max_split = plan.split;
   CUtensorMap mw, mx;
   const uint64_t wrows = static_cast<uint64_t>(out_features) * (gated ? 2 : 1);
   if (!make_map2(&mw, weight, fp8, in_features, wrows, static_cast<uint64_t>(in_features) * row_bytes, kTileM) ||
-      !make_map2(&mx, x, fp8, in_features, rows, static_cast<uint64_t>(x_stride) * row_bytes, p.bn))
+      !make_map2(&mx, x, fp8, in_features, rows, static_cast<uint64_t>(x_stride) * row_bytes, pair ? p.bn / 2 : p.bn))
     return MHC_ERR_CUDA;
-  if (fp8) return gated ? launch_gemm<true, true, kDense>(p, mw, mx, grid, stream)
-                        : launch_gemm<true, false, kDense>(p, mw, mx, grid, stream);
-  return gated ? launch_gemm<false, true, kDense>(p, mw, mx, grid, stream)
-               : launch_gemm<false, false, kDense>(p, mw, mx, grid, stream);
+  if (pair) return gated ? launch_pair<true, kDense>(p, mw, mx, stream) : launch_pair<false, kDense>(p, mw, mx, stream);
+  if (fp8) return gated ? launch_linear<true, true>(p, plan, mw, mx, stream)
+                        : launch_linear<true, false>(p, plan, mw, mx, stream);
+  return gated ? launch_linear<false, true>(p, plan, mw, mx, stream)
+               : launch_linear<false, false>(p, plan, mw, mx, stream);
 }
 
 size_t mhc_moe_experts_workspace_bytes(int rows, int num_permuted, int intermediate) {
   if (rows < 1 || rows > kMaxTokens || num_permuted < 1 || intermediate < 1) return 0;
-  return kGemmHeader + partial_bytes(rows) + static_cast<size_t>(num_permuted) * intermediate * 2;
+  return kGemmHeader + kPartialBytes + static_cast<size_t>(num_permuted) * intermediate * 2;
 }
 
 mhc_status mhc_moe_experts(const mhc_bf16* x, int64_t x_stride, const mhc_bf16* w13, const mhc_bf16* w2,
@@ -723,12 +1055,12 @@ mhc_status mhc_moe_experts(const mhc_bf16* x, int64_t x_stride, const mhc_bf16* 
       ws_bytes < mhc_moe_experts_workspace_bytes(rows, num_permuted, intermediate))
     return MHC_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
-  __nv_bfloat16* inner = reinterpret_cast<__nv_bfloat16*>(ws + kGemmHeader + partial_bytes(rows));
+  __nv_bfloat16* inner = reinterpret_cast<__nv_bfloat16*>(ws + kGemmHeader + kPartialBytes);
   GemmParams p{};
   p.rows = num_permuted;
   p.x_rows = rows;
   p.experts = experts;
-  p.max_split = kMaxSplit;
+  p.paired = 1;
   p.offsets = expert_offsets;
   p.prow = permuted_rows;
   p.status = reinterpret_cast<unsigned*>(ws);
@@ -740,7 +1072,13 @@ mhc_status mhc_moe_experts(const mhc_bf16* x, int64_t x_stride, const mhc_bf16* 
   const int mean = (num_permuted + experts - 1) / experts;
   int bn = mean <= 4 ? 16 : mean <= 16 ? 32 : mean <= 48 ? 64 : 128;
   if (bn > round16(rows)) bn = round16(rows);
+  const bool pair = mean > kPairMean;
+  if (pair) bn = 256;
   p.bn = bn;
+  p.k = hidden;
+  p.x = reinterpret_cast<const __nv_bfloat16*>(x);
+  p.x_stride = x_stride;
+  p.max_split = bn <= kSplitCols ? kMaxShares - 1 : 1;
   const int grid = gemm_grid();
   CUtensorMap mw, mx;
   // first product: gate and up rows of an expert's w13, token rows gathered
@@ -754,7 +1092,8 @@ mhc_status mhc_moe_experts(const mhc_bf16* x, int64_t x_stride, const mhc_bf16* 
                  static_cast<uint64_t>(hidden) * 2, kTileM) ||
       !make_map2(&mx, x, false, hidden, rows, static_cast<uint64_t>(x_stride) * 2, 1))
     return MHC_ERR_CUDA;
-  mhc_status st = launch_gemm<false, true, kGather>(p, mw, mx, grid, stream);
+  mhc_status st = pair ? launch_pair<true, kGather>(p, mw, mx, stream)
+                       : launch_gemm<false, true, kGather, 1>(p, mw, mx, grid, 1, stream);
   if (st != MHC_OK) return st;
   // second product: the intermediate rows as they lie
   p.n = hidden;
@@ -765,9 +1104,10 @@ mhc_status mhc_moe_experts(const mhc_bf16* x, int64_t x_stride, const mhc_bf16* 
   p.act = MHC_ACT_NONE;
   if (!make_map2(&mw, w2, false, intermediate, static_cast<uint64_t>(experts) * hidden,
                  static_cast<uint64_t>(intermediate) * 2, kTileM) ||
-      !make_map2(&mx, inner, false, intermediate, num_permuted, static_cast<uint64_t>(intermediate) * 2, p.bn))
+      !make_map2(&mx, inner, false, intermediate, num_permuted, static_cast<uint64_t>(intermediate) * 2, pair ? 16 : p.bn))
     return MHC_ERR_CUDA;
-  return launch_gemm<false, false, kGrouped>(p, mw, mx, grid, stream);
+  if (pair) return launch_pair<false, kGrouped>(p, mw, mx, stream);
+  return launch_gemm<false, false, kGrouped, 1>(p, mw, mx, grid, 1, stream);
 }
 
 }  // extern "C"

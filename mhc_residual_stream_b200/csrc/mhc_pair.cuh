@@ -1,0 +1,290 @@
+// The product of many token rows: two CTAs of a cluster (a pair of SMs) on one
+// tile. Included by mhc_gemm.cu, whose parameters, schedule and epilogue it uses.
+//
+// With one CTA per tile of 128 x 256 every K block brings 48 KB to an SM for 512
+// cycles of products; the SMs together then ask L2 for more than it gives (about
+// 14.5 TB/s, 52 bytes a cycle and SM, measured with every tile shape tried). A pair
+// computes 256 weight rows x up to 256 token rows: each CTA loads its 128 weight
+// rows (gated: 128 gate and 128 up rows) and half of the token rows, 32 KB per 512
+// cycles (gated: 48 KB per 1024), and the tensor cores of both SMs read the other
+// half from the neighbour's shared memory (tcgen05 cta_group::2). The accumulator
+// of a CTA's weight rows lies in its own tensor memory and its own warps finish it.
+//
+//   warp 0      each CTA: copies by tensor map, counted on the first CTA's barrier
+//   warp 1      first CTA: issues the products for both
+//   warps 2-5   each CTA: epilogue of its 128 weight rows
+//   warps 6-9   gathered token rows only: 16-byte asynchronous copies of the CTA's
+//               half of the rows, written in the swizzle the products read (the
+//               tensor-map gather moves four rows per 65 cycles, an eighth of what
+//               a tile of 128 columns needs)
+#pragma once
+
+namespace mhc {
+
+constexpr int kPairTileM = 256;
+constexpr int kPairLag = 2;  // gathered stages in flight behind the one being issued
+
+__device__ __forceinline__ void tmem_alloc2(unsigned* slot, unsigned cols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish2() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_dealloc2(unsigned addr, unsigned cols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
+}
+// As tma_load_2d, counted on a barrier of the pair (a shared::cluster address).
+__device__ __forceinline__ void tma_load_2d_pair(unsigned dst, const void* map, int x, int y, unsigned bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+// D[256 x N] (+)= A[256 x 16] B[N x 16]^T over the pair: each CTA holds 128 rows of A
+// and N / 2 rows of B at the same shared-memory addresses.
+__device__ __forceinline__ void mma_bf16_pair(unsigned d, unsigned a, unsigned b, unsigned idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "n"(kDescHi)
+      : "memory");
+}
+// Arrive on the barrier at this address in both CTAs once the products are done.
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(static_cast<unsigned short>(3))
+      : "memory");
+}
+// Arrive on a barrier of the cluster, releasing what this thread (and, ordered by a
+// warp barrier, its warp) wrote before.
+__device__ __forceinline__ void mbar_arrive_cluster(unsigned addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ void cp_async16_or_zero(unsigned dst, const void* src, bool has) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(has ? 16 : 0) : "memory");
+}
+
+template <bool GATED, int SRC>
+__global__ void __cluster_dims__(2) __launch_bounds__(SRC == kGather ? 320 : 192, 1)
+    pair_kernel(const __grid_constant__ GemmParams p, const __grid_constant__ CUtensorMap tm_w,
+                const __grid_constant__ CUtensorMap tm_x) {
+  extern __shared__ unsigned char raw[];
+  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
+  __shared__ unsigned tmem_slot;
+  constexpr int kAcc = GATED ? 2 : 1;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(kFull, tid >> 5, 0);  // uniform
+  const int rank = blockIdx.x & 1;
+  const int x_bytes = p.bn / 2 * 128;  // bn is a multiple of 32: whole 8-row swizzle groups
+  const unsigned smem0 = (smem_u32(raw) + 1023u) & ~1023u;
+  const unsigned x0 = smem0 + p.stages * (kAcc * kATile);
+  int* first = nullptr;
+  int* off = nullptr;
+  if constexpr (SRC != kDense) {
+    first = reinterpret_cast<int*>(raw + (x0 - smem_u32(raw)) + p.stages * x_bytes);
+    off = first + p.experts + 1;
+  }
+  if (tid == 0) {
+    prefetch_tensormap(&tm_w);
+    if (SRC != kGather) prefetch_tensormap(&tm_x);
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&full[i], SRC == kGather ? 1 + 8 : 1);  // the copies' bytes, and both CTAs' gathering warps
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 8);  // both CTAs' epilogue warps
+    }
+  }
+  if (warp == 1) {
+    tmem_alloc2(&tmem_slot, 512);
+    tmem_relinquish2();
+  }
+  int tiles;
+  if constexpr (SRC == kDense) {
+    tiles = p.m_tiles * ((p.rows + p.bn - 1) / p.bn);
+  } else {
+    if constexpr (SRC == kGather) griddep_wait();  // as in gemm_kernel
+    if (warp == 0) expert_tiles(p, first, off, lane);
+  }
+  tcgen05_fence_before();
+  __syncthreads();
+  tcgen05_fence_after();
+  cluster_arrive();
+  griddep_launch_dependents();
+  if constexpr (SRC != kDense) tiles = first[p.experts];
+  const unsigned tmem = tmem_slot;
+  cluster_wait();  // the other CTA's barriers are set
+
+  const int pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+  const int acc_cols = kAcc * p.bn;
+
+  if (warp == 0) {
+    // ------------------------------------------------ copies
+    const unsigned bar0 = cluster_address(smem_u32(&full[0]), 0);
+    if constexpr (SRC != kGather) griddep_wait();
+    int s = 0;
+    unsigned ph = 1;
+    bool ok = true;
+    for (int tile = pair; ok && tile < tiles; tile += pairs) {
+      const TileAt t = tile_even<SRC>(p, first, off, tile);
+      const int half = round32(t.ntok) / 2;
+      const int wrow = (SRC == kDense ? 0 : t.expert * (kAcc * p.n)) + t.m * kPairTileM + rank * kTileM;
+      const int xrow = t.tok0 + rank * half;
+      const unsigned bytes = kAcc * kATile + (SRC == kDense ? x_bytes : SRC == kGrouped ? half * 128 : 0);
+      for (int kb = 0; kb < p.kblocks; ++kb) {
+        if (!(ok = __all_sync(kFull, wait_for_cluster(&empty[s], ph, p)))) break;
+        if (elect_one()) {
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * bytes + p.extra_tx);
+          const unsigned bar = bar0 + s * 8, dst = smem0 + s * (kAcc * kATile), xdst = x0 + s * x_bytes;
+          tma_load_2d_pair(dst, &tm_w, kb * 64, wrow, bar);
+          if constexpr (GATED) tma_load_2d_pair(dst + kATile, &tm_w, kb * 64, wrow + p.n, bar);
+          if constexpr (SRC == kDense) tma_load_2d_pair(xdst, &tm_x, kb * 64, xrow, bar);
+          if constexpr (SRC == kGrouped)
+            for (int r = 0; r < half; r += 16) tma_load_2d_pair(xdst + r * 128, &tm_x, kb * 64, xrow + r, bar);
+        }
+        __syncwarp();
+        if (++s == p.stages) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+    }
+    if (!ok) {  // leave no copy in flight behind
+      const long long until = clock64() + 200000;
+      while (clock64() < until) __nanosleep(1000);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------ products
+    if (rank == 0) {
+      const unsigned a_lo = desc_lo(smem0), b_lo = desc_lo(x0);
+      int s = 0, buf = 0;
+      unsigned ph = 0, aph = 1;
+      bool ok = true;
+      for (int tile = pair; ok && tile < tiles; tile += pairs) {
+        const TileAt t = tile_even<SRC>(p, first, off, tile);
+        const unsigned idesc = p.idesc | (static_cast<unsigned>(round32(t.ntok) >> 3) << 17);
+        if (!(ok = __all_sync(kFull, wait_for_cluster(&acc_empty[buf], aph, p)))) break;
+        tcgen05_fence_after();
+        const unsigned d = tmem + buf * acc_cols;
+        for (int kb = 0; kb < p.kblocks; ++kb) {
+          if (!(ok = __all_sync(kFull, wait_for_cluster(&full[s], ph, p)))) break;
+          tcgen05_fence_after();
+          if (elect_one()) {
+            const unsigned a = a_lo + s * (kAcc * kATile / 16), b = b_lo + s * (x_bytes / 16);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int q = 0; q < kAcc; ++q)
+                mma_bf16_pair(d + q * p.bn, a + q * (kATile / 16) + 2 * k, b + 2 * k, idesc, k > 0 || kb > 0);
+            mma_commit_pair(&empty[s]);
+            if (kb == p.kblocks - 1) mma_commit_pair(&acc_full[buf]);
+          }
+          __syncwarp();
+          if (++s == p.stages) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+        if (!ok) break;
+        if (++buf == p.nbuf) {
+          buf = 0;
+          aph ^= 1;
+        }
+      }
+    }
+  } else if (warp < 6) {
+    // ------------------------------------------------ epilogue
+    if constexpr (SRC != kGather) griddep_wait();
+    const int q = warp & 3;
+    int buf = 0;
+    unsigned ph = 0;
+    for (int tile = pair; tile < tiles; tile += pairs) {
+      const TileAt t = tile_even<SRC>(p, first, off, tile);
+      const int f = t.m * kPairTileM + rank * kTileM + q * 32 + lane;
+      float bg = 0.f, bu = 0.f;
+      if (p.bias != nullptr && f < p.n) {
+        bg = p.bias[f];
+        if constexpr (GATED) bu = p.bias[p.n + f];
+      }
+      if (!epilogue_all(wait_for_cluster(&acc_full[buf], ph, p))) break;
+      tcgen05_fence_after();
+      const unsigned src = tmem + buf * acc_cols + (static_cast<unsigned>(q * 32) << 16);
+      for (int c = 0; c < t.ntok; c += 16) {
+        float v[16], u[16];
+        read_sums<GATED>(src + c, p.bn, v, u);
+        store_columns<GATED, 16>(p, v, u, bg, bu, t.tok0 + c, f, t.ntok - c);
+      }
+      tcgen05_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(cluster_address(smem_u32(&acc_empty[buf]), 0));
+      if (++buf == p.nbuf) {
+        buf = 0;
+        ph ^= 1;
+      }
+    }
+  } else if constexpr (SRC == kGather) {
+    // ------------------------------------------------ gathered token rows
+    const int g = tid - 192, col = g & 7, r0 = g >> 3;  // 16-byte column; rows r0, r0 + 16, ...
+    const unsigned bar0 = cluster_address(smem_u32(&full[0]), 0);
+    const unsigned dst0 = x0 + r0 * 128 + ((col ^ (r0 & 7)) << 4);
+    int s = 0, i = 0, told = 0;  // stage, stages issued, stages reported
+    unsigned ph = 1;
+    bool ok = true;
+    auto report = [&]() {  // the oldest unreported stage has landed
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(bar0 + (told % p.stages) * 8);
+      ++told;
+    };
+    for (int tile = pair; ok && tile < tiles; tile += pairs) {
+      const TileAt t = tile_even<SRC>(p, first, off, tile);
+      const int half = round32(t.ntok) / 2;
+      const __nv_bfloat16* row[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int c = rank * half + r0 + 16 * j;
+        int r = r0 + 16 * j < half && c < t.ntok ? p.prow[t.tok0 + c] : 0;
+        if (r < 0 || r >= p.x_rows) {
+          record_error(p.status, MHC_ERR_DEVICE_INDEX);
+          r = 0;
+        }
+        row[j] = p.x + r * p.x_stride + col * 8;
+      }
+      for (int kb = 0; kb < p.kblocks; ++kb) {
+        if (!(ok = __all_sync(kFull, wait_for_cluster(&empty[s], ph, p)))) break;
+        const unsigned dst = dst0 + s * x_bytes;
+        const bool has = kb * 64 + col * 8 < p.k;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (16 * j < half) cp_async16_or_zero(dst + j * 2048, row[j] + (has ? kb * 64 : 0), has);
+        cp_async_commit();
+        if (++i - told > kPairLag) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(kPairLag) : "memory");
+          report();
+        }
+        if (++s == p.stages) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+    }
+    cp_async_wait_all();
+    while (told < i) report();
+  }
+  tcgen05_fence_before();
+  __syncthreads();
+  cluster_arrive();
+  cluster_wait();  // the pair's products are done and nobody will arrive here any more
+  if (warp == 1) {
+    tcgen05_fence_after();
+    tmem_dealloc2(tmem, 512);
+  }
+}
+
+}  // namespace mhc

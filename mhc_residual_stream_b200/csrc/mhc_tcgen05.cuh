@@ -6,6 +6,15 @@
 
 namespace mhc {
 
+// One lane of the converged warp, the same one every time. The issuing loops run in
+// all lanes and elect at the instruction: their operands then stay in uniform
+// registers (a K block issued inside an `if (lane == 0)` took 685 cycles).
+__device__ __forceinline__ bool elect_one() {
+  unsigned r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 // ---------------------------------------------------------------- tensor-map copies (this GPU's memory)
 
 __device__ __forceinline__ void tma_load_2d(unsigned dst, const void* map, int x, int y, uint64_t* bar) {
@@ -60,34 +69,37 @@ __device__ __forceinline__ void tcgen05_fence_after() { asm volatile("tcgen05.fe
 // ---------------------------------------------------------------- MMA (one issuing thread)
 
 // Shared-memory operand descriptor of a K-major tile of 128-byte rows in the
-// 128-byte swizzle (8-row groups 1024 bytes apart); addr 1024-byte aligned, plus
-// the byte offset of the K step within the row.
-__device__ __forceinline__ uint64_t desc_sw128(unsigned addr) {
-  return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-}
+// 128-byte swizzle (8-row groups 1024 bytes apart): the high word is the same for
+// every tile, the low word takes the address (1024-byte aligned, plus 32 bytes per
+// K step within the row: 2 units).
+constexpr unsigned kDescHi = 64u | (1u << 14) | (2u << 29);
+__device__ __forceinline__ unsigned desc_lo(unsigned addr) { return ((addr & 0x3ffffu) >> 4) | (1u << 16); }
 // Descriptor of a 512-byte scale tile (32 rows of 16 bytes, 8-row groups 128
 // bytes apart, no swizzle).
 __device__ __forceinline__ uint64_t desc_scales(unsigned addr) {
   return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (8ull << 32) | (1ull << 46);
 }
 
-// D[128 x N] (+)= A[128 x 16] B[N x 16]^T, bf16 operands, fp32 accumulator.
-__device__ __forceinline__ void mma_bf16(unsigned d, uint64_t a, uint64_t b, unsigned idesc, bool accumulate) {
+// D[128 x N] (+)= A[128 x 16] B[N x 16]^T, bf16 operands (low descriptor words),
+// fp32 accumulator.
+__device__ __forceinline__ void mma_bf16(unsigned d, unsigned a, unsigned b, unsigned idesc, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "n"(kDescHi)
       : "memory");
 }
 // D[128 x N] (+)= A[128 x 32] B[N x 32]^T, E4M3 operands with one E8M0 scale per
 // row and 32 elements (tensor memory at sa, sb; the byte is in idesc).
-__device__ __forceinline__ void mma_mxf8(unsigned d, uint64_t a, uint64_t b, unsigned idesc, unsigned sa, unsigned sb,
+__device__ __forceinline__ void mma_mxf8(unsigned d, unsigned a, unsigned b, unsigned idesc, unsigned sa, unsigned sb,
                                          bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "mov.b64 da, {%1, %7};\n\tmov.b64 db, {%2, %7};\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], da, db, %3, [%5], [%6], p;\n\t}" ::"r"(
           d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(sa), "r"(sb)
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(sa), "r"(sb), "n"(kDescHi)
       : "memory");
 }
 // A 512-byte scale tile into 4 columns of tensor memory, the 32 lanes repeated in
@@ -99,6 +111,19 @@ __device__ __forceinline__ void tmem_copy_scales(unsigned addr, uint64_t desc) {
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
+}
+
+// mbar_try_wait on a barrier that other CTAs of the cluster arrive on.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, unsigned parity) {
+  unsigned ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {

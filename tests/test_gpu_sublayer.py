@@ -45,6 +45,9 @@ LINEAR = [  # rows, K, N, activation, bias, residual, out
     (300, 24, 2000, "relu", False, False, torch.bfloat16),
     (1030, 192, 1100, "none", False, True, torch.float32),
     (4099, 64, 64, "gelu", True, False, torch.bfloat16),
+    (193, 72, 513, "swiglu", True, True, torch.bfloat16),
+    (1000, 136, 300, "swiglu", False, False, torch.float32),
+    (2500, 320, 777, "silu", True, False, torch.float32),
 ]
 
 
@@ -333,7 +336,7 @@ def run_experts(x, w13, w2, prow, off, out=None, workspace=None):
 @pytest.mark.parametrize("R,k,E,H,I", [
     (1, 1, 1, 8, 8), (1, 8, 64, 256, 128), (1, 2, 4, 2048, 136), (7, 3, 5, 72, 40), (16, 4, 16, 512, 264),
     (37, 3, 24, 712, 328), (50, 8, 8, 192, 200), (128, 8, 32, 320, 72), (200, 2, 3, 136, 304), (700, 4, 6, 64, 128),
-    (20, 2, 300, 64, 16), (9, 16, 1000, 64, 8),
+    (20, 2, 300, 64, 16), (9, 16, 1000, 64, 8), (513, 4, 5, 200, 136), (1500, 2, 2, 72, 520), (2000, 3, 16, 128, 264),
 ])
 def test_experts(R, k, E, H, I):
     x, w13, w2, e2p, prow, off = draw_experts(R, k, E, H, I, seed=R + E)
@@ -344,7 +347,7 @@ def test_experts(R, k, E, H, I):
     assert torch.equal(out, again) and M.mhc_get_device_status(ws) == M.OK
 
 
-@pytest.mark.parametrize("R,k", [(40, 4), (300, 2)])
+@pytest.mark.parametrize("R,k", [(40, 4), (300, 2), (1100, 2)])
 def test_experts_of_one_popular_expert_and_unused_places(R, k):
     E, H, I = 12, 200, 136
     ids = np.full((R, k), -1)
@@ -369,17 +372,19 @@ def test_experts_strided_rows():
     assert torch.equal(out, run_experts(x, w13, w2, prow, off)[0])
 
 
-def test_experts_report_bad_indices():
-    x, w13, w2, e2p, prow, off = draw_experts(30, 2, 6, 128, 64, seed=3)
+@pytest.mark.parametrize("R", [30, 600])
+def test_experts_report_bad_indices(R):
+    x, w13, w2, e2p, prow, off = draw_experts(R, 2, 6, 128, 64, seed=3)
     good, _ = run_experts(x, w13, w2, prow, off)
-    for bad in (30, -1, 1 << 30):  # a row that x does not have reads row 0
+    for bad in (R, -1, 1 << 30):  # a row that x does not have reads row 0
         p = prow.copy()
         p[11] = bad
         out, ws = run_experts(x, w13, w2, p, off)
         assert M.mhc_get_device_status(ws) == M.DEVICE_INDEX
-        keep = [i for i in range(60) if i != 11]
+        keep = [i for i in range(2 * R) if i != 11]
         assert torch.equal(out[keep], good[keep])
-    for o in ([0, 10, 5, 20, 30, 40, 60], [0, 10, 20, 30, 40, 50, 61], [-1, 10, 20, 30, 40, 50, 60]):
+    n = 2 * R
+    for o in ([0, 10, 5, 20, 30, 40, n], [0, 10, 20, 30, 40, 50, n + 1], [-1, 10, 20, 30, 40, 50, n]):
         out, ws = run_experts(x, w13, w2, prow, np.array(o))  # nothing is computed
         assert M.mhc_get_device_status(ws) == M.DEVICE_INDEX
         assert bool((out == 5.0).all())

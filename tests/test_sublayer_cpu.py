@@ -88,7 +88,7 @@ def test_experts_refusals(L):
 
 def test_workspace_sizes(L):
     sizes = [M.mhc_linear_workspace_bytes(r) for r in (1, 16, 17, 100, 127, 128, 300, 65535)]
-    assert sizes == sorted(sizes) and sizes[0] > 2048
+    assert sizes == sorted(sizes) and sizes[0] >= 2048
     for bad in (0, -1, 65536):
         assert M.mhc_linear_workspace_bytes(bad) == 0
     assert M.mhc_moe_experts_workspace_bytes(4, 32, 128) >= M.mhc_linear_workspace_bytes(4) + 32 * 128 * 2
