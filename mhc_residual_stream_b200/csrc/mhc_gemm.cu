@@ -61,9 +61,6 @@ enum Source { kDense = 0, kGather = 1, kGrouped = 2 };
 
 struct GemmParams {
   int rows;      // token rows of x (dense), permuted rows (grouped)
-  int k;         // K (pair kernel, gathered rows)
-  const __nv_bfloat16* x;  // and those rows, x_stride elements apart
-  int64_t x_stride;
   int x_rows;    // rows that may be gathered
   int n;         // output features
   int kblocks;   // K in blocks of 128 bytes
@@ -72,6 +69,9 @@ struct GemmParams {
   unsigned idesc;
   const int32_t* offsets;  // [experts + 1]
   const int32_t* prow;     // source row of each permuted row
+  const __nv_bfloat16* x;  // permute_rows_kernel: rows of k elements, x_stride apart
+  int64_t x_stride;
+  int k;
   const uint8_t* x_scale;
   const uint8_t* w_scale;
   const float* bias;
@@ -282,12 +282,13 @@ __device__ __forceinline__ unsigned cluster_address(unsigned addr, int rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-// 16 bytes into the shared memory of a CTA of the cluster, counted on its barrier.
-__device__ __forceinline__ void st_async4(unsigned addr, const float* v, unsigned bar) {
-  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1,%2,%3,%4}, [%5];" ::"r"(addr),
-               "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "r"(bar)
+// Shared memory to the shared memory of a CTA of the cluster, counted on its barrier.
+__device__ __forceinline__ void bulk_s2cluster(unsigned dst, unsigned src, unsigned bytes, unsigned bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "r"(src), "r"(bytes), "r"(bar)
                : "memory");
 }
+
 __device__ __forceinline__ float silu(float v) { return v / (1.f + __expf(-v)); }
 
 // C token columns of a warp's 32 output features (thread: feature f), from the
@@ -380,6 +381,75 @@ __device__ __forceinline__ void add4(float (&v)[4], const float4 a) {
   v[3] += a.w;
 }
 
+// The epilogue of a tile that a cluster computes, K divided over its CTAs: token
+// column c is finished by CTA c / each. A CTA lays its sums out by that CTA in its
+// drained ring, [CTA][gate, up][column / 4][feature][4], and one bulk copy per CTA
+// takes them there; the columns that arrive are added in CTA order, which is K
+// order. (Threads storing the sums remotely took 120 cycles per 512 bytes.)
+template <bool GATED>
+__device__ __forceinline__ void finish_in_cluster(const GemmParams& p, const Schedule& sched, unsigned char* raw,
+                                                  unsigned smem0, unsigned sums0, unsigned tmem, uint64_t* acc_full,
+                                                  uint64_t* sums_in, int q, int lane) {
+  constexpr int kAcc = GATED ? 2 : 1;
+  const int S = p.max_split, r = sched.cta % S;
+  const TileAt t = tile_at<kDense>(p, nullptr, nullptr, sched.cta / S);
+  const int each = columns_each(t.ntok, S), n = min(each, t.ntok - r * each);
+  const int owners = (t.ntok + each - 1) / each;
+  const int row = q * 32 + lane, f = t.m * kTileM + row;
+  const unsigned block = kAcc * each * kTileM * 4;  // bytes of the sums for one CTA
+  const unsigned peer = min(lane, S - 1);
+  const unsigned dst = cluster_address(sums0 + r * block, peer), bar = cluster_address(smem_u32(sums_in), peer);
+  float bg = 0.f, bu = 0.f;
+  if (p.bias != nullptr && f < p.n) {
+    bg = p.bias[f];
+    if constexpr (GATED) bu = p.bias[p.n + f];
+  }
+  unsigned char* out = raw + (smem0 - smem_u32(raw)) + row * 16;
+  const bool ok = epilogue_all(wait_for(&acc_full[0], 0, p));
+  if (ok) {
+    tcgen05_fence_after();
+    const unsigned src = tmem + (static_cast<unsigned>(q * 32) << 16);
+    int at = 0;
+    unsigned to = 0;  // offset of the CTA's block
+    for (int c = 0; c < t.ntok; c += 16) {
+      float v[16], u[16];
+      read_sums<GATED>(src + c, p.bn, v, u);
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        if (c + i < t.ntok) {
+          *reinterpret_cast<float4*>(out + to + at * (kTileM * 4)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          if constexpr (GATED)
+            *reinterpret_cast<float4*>(out + to + (each + at) * (kTileM * 4)) =
+                make_float4(u[i], u[i + 1], u[i + 2], u[i + 3]);
+          if ((at += 4) == each) {
+            at = 0;
+            to += block;
+          }
+        }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    epilogue_barrier();
+  }
+  cluster_wait();  // every CTA of the cluster runs and its barriers are set
+  if (ok && q == 2 && lane < owners) bulk_s2cluster(dst, smem0 + lane * block, block, bar);
+  __syncwarp();
+  if (ok && n > 0 && __all_sync(kFull, wait_for_cluster(sums_in, 0, p))) {
+    const float4* from = reinterpret_cast<const float4*>(raw + (sums0 - smem_u32(raw))) + row;
+    for (int c = 0; c < n; c += 4) {
+      float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+      for (int k = 0; k < S; ++k) {
+        const float4* a = from + (k * kAcc * each + c) / 4 * kTileM;
+        add4(v, a[0]);
+        if constexpr (GATED) add4(u, a[each / 4 * kTileM]);
+      }
+      store_columns<GATED, 4>(p, v, u, bg, bu, t.tok0 + r * each + c, f, n - c);
+    }
+  }
+  __syncwarp();
+  cluster_arrive();  // what was sent to this CTA is there
+}
+
 // ---------------------------------------------------------------- kernel
 
 template <bool FP8, bool GATED, int SRC, int CTAS>
@@ -446,8 +516,7 @@ __global__ void __launch_bounds__(kGemmThreads, CTAS)
     if (tid == 0) {  // the sums that the cluster will send for this CTA's columns
       const TileAt t = tile_at<SRC>(p, first, off, blockIdx.x / p.max_split);
       const int r = blockIdx.x % p.max_split, each = columns_each(t.ntok, p.max_split);
-      const int fours = (min(each, max(0, t.ntok - r * each)) + 3) / 4;
-      mbar_arrive_expect_tx(&sums_in, static_cast<unsigned>(fours) * 4 * kAcc * p.max_split * kTileM * 4);
+      mbar_arrive_expect_tx(&sums_in, r * each < t.ntok ? p.max_split * (kAcc * each * kTileM * 4) : 0);
     }
     __syncwarp();
     cluster_arrive();  // this CTA runs and its barriers are set
@@ -611,12 +680,12 @@ __global__ void __launch_bounds__(kGemmThreads, CTAS)
     // ------------------------------------------------ epilogue
     if constexpr (SRC != kGather) griddep_wait();
     const int q = warp & 3;  // the quarter of the accumulator's lanes this warp can read
+    if (clustered) finish_in_cluster<GATED>(p, sched, raw, smem0, sums0, tmem, acc_full, &sums_in, q, lane);
     Segments it(sched);
     Segment g;
     int buf = 0;
     unsigned ph = 0;
-    bool sent = false;
-    while (it.next(g)) {
+    while (!clustered && it.next(g)) {
       const TileAt t = tile_at<SRC>(p, first, off, g.tile);
       const int f = t.m * kTileM + q * 32 + lane;
       float bg = 0.f, bu = 0.f;
@@ -629,33 +698,6 @@ __global__ void __launch_bounds__(kGemmThreads, CTAS)
       const unsigned src = tmem + buf * acc_cols + (static_cast<unsigned>(q * 32) << 16);
       const bool whole = g.k0 == 0 && g.k1 == p.kblocks;
       const size_t slot_floats = static_cast<size_t>(kAcc) * p.bn * kTileM;
-      if (clustered) {
-        // token column c is finished by CTA c / each of the cluster; a thread sends four
-        // columns at a time (columns behind the last are sent and not used)
-        const int S = p.max_split, each = columns_each(t.ntok, S);
-        const unsigned mine_at = sums0 + (sched.cta % S) * (kAcc * each * kTileM * 4) + (q * 32 + lane) * 16;
-        cluster_wait();
-        int owner = 0, at = 0;
-        unsigned dst = cluster_address(mine_at, 0), bar = cluster_address(smem_u32(&sums_in), 0);
-        for (int c = 0; c < t.ntok; c += 16) {
-          float v[16], u[16];
-          read_sums<GATED>(src + c, p.bn, v, u);
-#pragma unroll
-          for (int i = 0; i < 16; i += 4)
-            if (c + i < t.ntok) {
-              st_async4(dst + at * (kTileM * 4), v + i, bar);
-              if constexpr (GATED) st_async4(dst + (each + at) * (kTileM * 4), u + i, bar);
-              if ((at += 4) == each) {
-                at = 0;
-                owner = min(owner + 1, S - 1);
-                dst = cluster_address(mine_at, owner);
-                bar = cluster_address(smem_u32(&sums_in), owner);
-              }
-            }
-        }
-        sent = true;
-        break;
-      }
       // partial sums of a shared tile in the workspace, [column][feature]
       float* slot = p.partials + (static_cast<size_t>(sched.cta) * 2 + (g.k0 > 0 ? 0 : 1)) * slot_floats + q * 32 + lane;
       for (int c = 0; c < t.ntok; c += 16) {
@@ -718,33 +760,6 @@ __global__ void __launch_bounds__(kGemmThreads, CTAS)
               if constexpr (GATED) u[0][i] += u[k][i];
             }
           store_columns<GATED, 4>(p, v[0], u[0], bg, bu, t.tok0 + c, f, t.ntok - c);
-        }
-      }
-    }
-    if (clustered) {
-      __syncwarp();
-      if (!sent) cluster_wait();
-      cluster_arrive();
-      const bool in = sent && wait_for_cluster(&sums_in, 0, p);
-      if (in) {
-        const int S = p.max_split, r = sched.cta % S;
-        const TileAt t = tile_at<SRC>(p, first, off, sched.cta / S);
-        const int row = q * 32 + lane, f = t.m * kTileM + row;
-        float bg = 0.f, bu = 0.f;
-        if (p.bias != nullptr && f < p.n) {
-          bg = p.bias[f];
-          if constexpr (GATED) bu = p.bias[p.n + f];
-        }
-        const int each = columns_each(t.ntok, S), n = min(each, t.ntok - r * each);
-        const float4* from = reinterpret_cast<const float4*>(raw + (sums0 - smem_u32(raw))) + row;
-        for (int c = 0; c < n; c += 4) {
-          float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-          for (int k = 0; k < S; ++k) {
-            add4(v, from[(k * kAcc * each + c) / 4 * kTileM]);
-            if constexpr (GATED) add4(u, from[((k * kAcc + 1) * each + c) / 4 * kTileM]);
-          }
-          store_columns<GATED, 4>(p, v, u, bg, bu, t.tok0 + r * each + c, f, n - c);
         }
       }
     }
@@ -862,6 +877,7 @@ int round16(int v) { return (v + 15) / 16 * 16; }
 
 struct Plan {
   int bn, split, per_sm, grid;
+  bool pair;
 };
 
 // CTAs that are resident at once in clusters of 1..16, at one and two CTAs an SM,
@@ -870,26 +886,39 @@ struct Plan {
 constexpr int kRoom[2][16] = {{148, 148, 135, 132, 130, 132, 105, 120, 108, 110, 99, 84, 91, 98, 105, 112},
                               {296, 296, 279, 284, 280, 270, 259, 264, 243, 260, 253, 252, 234, 224, 210, 224}};
 
-// Token columns of a tile and CTAs per tile of a dense product: the least of a
-// simple estimate of the time, in SM cycles. A K block costs the larger of its
-// products (128 x bn x 64 bf16 multiply-adds at 4096 a cycle) and its copies (what
-// the ring holds, once per memory latency, at most kCopyRate bytes a cycle and SM
-// and the memory's rate over all SMs); a tile adds its epilogue.
+// Token columns of a tile and CTAs per tile of a dense product: the least of an
+// estimate of the time, in SM cycles, over a few candidates. Its constants fit the
+// times of 27 products (1-2048 rows, K 512-7168, 128-16000 features, plain, gated
+// and MXFP8) with every candidate; the candidate it picks takes 1.9% more than the
+// best one on average, 19% more at worst. A K block costs the largest of
+//   its products, 128 x bn x 64 multiply-adds at 4096 a cycle;
+//   kIssue, the least a K block takes on one SM (its copies, waits and issue);
+//   its copies: what the ring holds per kLatency, at most kCopyRate bytes a cycle on
+//   an SM and kL2Rate over all of them.
+// A tile adds kEpilogue cycles a column, shared by a cluster kJoin + kJoinColumn a
+// column. A pair of CTAs (mhc_pair.cuh) halves the token rows that each copies.
 Plan plan_linear(const GemmParams& p, int rows, bool fp8, bool gated) {
-  constexpr double kCopyRate = 60, kLatency = 2400, kMemoryRate = 3500, kTileCost = 2500;
+  constexpr double kLatency = 2300, kCopyRate = 66, kL2Rate = 7700, kIssue = 510, kEpilogue = 19, kJoin = 630,
+                   kJoinColumn = 125;
+  constexpr int kSplits[] = {1, 2, 3, 4, 5, 6, 8, 12, 16};
   const int sms = gemm_grid();
   const int acc = gated ? 2 : 1;
   const int cap = fp8 || gated ? 128 : 256;
-  Plan best{0, 1, 1, 1};
+  const int most = round16(rows < cap ? rows : cap);
+  Plan best{0, 1, 1, 1, false};
   double least = 0;
-  for (int bn = round16(rows < cap ? rows : cap); bn >= 16; bn -= 16) {
+  for (int c = 0; c < 6; ++c) {
+    const int bn = c == 0 ? most : 8 << c;  // 16, 32, 64, 128, 256
+    if (c > 0 && bn >= most) break;
     if (fp8 && rows > bn && bn != 128) continue;  // a token tile starts at a scale tile's first row
     const int tiles = p.m_tiles * ((rows + bn - 1) / bn);
     const int stage = acc * kATile + bn * 128 + (fp8 ? (acc + 1) * 512 : 0);
     const int cols = acc * bn + (fp8 ? kMaxStages * (acc + 1) * 4 : 0);
+    const double bytes = acc * kATile + bn * 128;
     for (int per_sm = 1; per_sm <= 2; ++per_sm) {
-      for (int split = 1; split <= kMaxCluster && split <= p.kblocks; ++split) {
-        if (split > 1 && tiles * split > kRoom[per_sm - 1][split - 1]) continue;
+      for (int split : kSplits) {
+        if (split > p.kblocks || tiles * split > (split > 1 ? kRoom[per_sm - 1][split - 1] : 1 << 30)) break;
+        if (split == 1 && per_sm == 2) continue;
         const int room = (per_sm == 2 ? kHalfSmem : kGemmSmem - kStaticSmem) - 1024 -
                          (split > 1 ? sums_bytes(bn, acc, split) : 0);
         int stages = room / stage < kMaxStages ? room / stage : kMaxStages;
@@ -897,31 +926,35 @@ Plan plan_linear(const GemmParams& p, int rows, bool fp8, bool gated) {
         const int ctas = split > 1 ? tiles * split : (tiles < sms ? tiles : sms);
         const int waves = split > 1 ? 1 : (tiles + sms - 1) / sms;
         const int blocks = (p.kblocks + split - 1) / split;
-        if (stages > blocks) stages = blocks;
+        if (waves == 1 && stages > blocks) stages = blocks;
         const double shared = ctas > sms ? static_cast<double>(ctas) / sms : 1.0;  // CTAs on one SM
-        const double bytes = acc * kATile + bn * 128;
         double rate = stages * bytes / kLatency;
         if (rate > kCopyRate / shared) rate = kCopyRate / shared;
-        if (rate > kMemoryRate / ctas) rate = kMemoryRate / ctas;
-        const double products = 2.0 * acc * bn * shared;
-        const double block = products > bytes / rate ? products : bytes / rate;
-        // a cluster's epilogue: its sums sent, and its columns finished
-        const double join = split > 1 ? 600 + 12.0 * acc * bn + 60.0 * columns_each(bn, split) : 24.0 * acc * bn;
-        const double t = waves * blocks * block + kTileCost + join;
+        if (rate > kL2Rate / ctas) rate = kL2Rate / ctas;
+        double block = (2.0 * acc * bn > kIssue ? 2.0 * acc * bn : kIssue) * shared;
+        if (block < bytes / rate) block = bytes / rate;
+        const double t = waves * blocks * block +
+                         (split > 1 ? kJoin + kJoinColumn * acc * bn : kEpilogue * acc * bn);
         if (best.bn == 0 || t < least) {
           least = t;
-          best = Plan{bn, split, split > 1 ? per_sm : 1, ctas};
+          best = Plan{bn, split, per_sm, ctas, false};
         }
       }
     }
   }
+  if (!fp8 && rows > 64) {
+    const int bn = rows < 256 ? round32(rows) : 256;
+    const int waves = ((p.n + kPairTileM - 1) / kPairTileM * ((rows + bn - 1) / bn) + sms / 2 - 1) / (sms / 2);
+    const double copies = (acc * kATile + bn / 2 * 128) / (kL2Rate / sms), products = 2.0 * acc * bn;
+    double block = copies > products ? copies : products;
+    if (block < kIssue) block = kIssue;
+    if (waves * p.kblocks * block + kEpilogue * acc * bn < least) best = Plan{bn, 1, 1, sms / 2 * 2, true};
+  }
   return best;
 }
 
-// Whether the pair kernel takes a product: enough token rows to be bound by the
-// tensor cores or L2 rather than by reading the weights once.
-constexpr int kPairRows = 192;   // of a dense product
-constexpr int kPairMean = 96;    // of an expert, on average
+// Whether the experts' products take the pair kernel: rows of an expert, on average.
+constexpr int kPairMean = 96;
 
 template <bool GATED, int SRC>
 mhc_status launch_pair(GemmParams& p, const CUtensorMap& w, const CUtensorMap& x, cudaStream_t stream) {
@@ -931,7 +964,7 @@ mhc_status launch_pair(GemmParams& p, const CUtensorMap& w, const CUtensorMap& x
   p.stages = (kGemmSmem - kStaticSmem - fixed) / stage;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   p.nbuf = 2 * acc * p.bn <= 512 ? 2 : 1;
-  if (p.stages <= kPairLag || p.bn % 32 != 0 || acc * p.bn > 512) return MHC_ERR_UNSUPPORTED_SHAPE;
+  if (p.stages < 2 || p.bn % 32 != 0 || acc * p.bn > 512) return MHC_ERR_UNSUPPORTED_SHAPE;
   p.m_tiles = (p.n + kPairTileM - 1) / kPairTileM;
   p.idesc = (static_cast<unsigned>(kPairTileM >> 4) << 24) | (1u << 4) | (1u << 7) | (1u << 10);
   p.budget_ns = g_budget_ns;
@@ -953,7 +986,7 @@ mhc_status launch_pair(GemmParams& p, const CUtensorMap& w, const CUtensorMap& x
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(gemm_grid() / 2 * 2);
-  cfg.blockDim = dim3(SRC == kGather ? 320 : 192);
+  cfg.blockDim = dim3(kGemmThreads);
   cfg.dynamicSmemBytes = fixed + p.stages * stage;
   cfg.stream = stream;
   cfg.attrs = attr;
@@ -1019,8 +1052,8 @@ mhc_status mhc_linear(const void* x, const uint8_t* x_scale, int64_t x_stride, c
              residual_stride % 2 == 0;
   p.status = static_cast<unsigned*>(workspace);
   const Plan plan = plan_linear(p, rows, fp8, gated);
-  const bool pair = !fp8 && rows > kPairRows && plan.split == 1;
-  p.bn = pair ? 256 : plan.bn;
+  const bool pair = plan.pair;
+  p.bn = plan.bn;
   p.max_split = plan.split;
   CUtensorMap mw, mx;
   const uint64_t wrows = static_cast<uint64_t>(out_features) * (gated ? 2 : 1);
@@ -1089,11 +1122,32 @@ mhc_status mhc_moe_experts(const mhc_bf16* x, int64_t x_stride, const mhc_bf16* 
   p.out_stride = intermediate;
   p.act = MHC_ACT_SWIGLU;
   if (!make_map2(&mw, w13, false, hidden, static_cast<uint64_t>(experts) * 2 * intermediate,
-                 static_cast<uint64_t>(hidden) * 2, kTileM) ||
-      !make_map2(&mx, x, false, hidden, rows, static_cast<uint64_t>(x_stride) * 2, 1))
+                 static_cast<uint64_t>(hidden) * 2, kTileM))
     return MHC_ERR_CUDA;
-  mhc_status st = pair ? launch_pair<true, kGather>(p, mw, mx, stream)
-                       : launch_gemm<false, true, kGather, 1>(p, mw, mx, grid, 1, stream);
+  mhc_status st;
+  if (pair) {
+    // the permuted rows stand in gemm2_permuted until the second product writes it
+    if (!make_map2(&mx, gemm2_permuted, false, hidden, num_permuted, static_cast<uint64_t>(hidden) * 2, 16))
+      return MHC_ERR_CUDA;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid * 8);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, permute_rows_kernel, p, reinterpret_cast<__nv_bfloat16*>(gemm2_permuted)) !=
+        cudaSuccess) {
+      (void)cudaGetLastError();
+      return MHC_ERR_CUDA;
+    }
+    st = launch_pair<true, kGrouped>(p, mw, mx, stream);
+  } else {
+    if (!make_map2(&mx, x, false, hidden, rows, static_cast<uint64_t>(x_stride) * 2, 1)) return MHC_ERR_CUDA;
+    st = launch_gemm<false, true, kGather, 1>(p, mw, mx, grid, 1, stream);
+  }
   if (st != MHC_OK) return st;
   // second product: the intermediate rows as they lie
   p.n = hidden;

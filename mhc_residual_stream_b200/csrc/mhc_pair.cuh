@@ -13,16 +13,16 @@
 //   warp 0      each CTA: copies by tensor map, counted on the first CTA's barrier
 //   warp 1      first CTA: issues the products for both
 //   warps 2-5   each CTA: epilogue of its 128 weight rows
-//   warps 6-9   gathered token rows only: 16-byte asynchronous copies of the CTA's
-//               half of the rows, written in the swizzle the products read (the
-//               tensor-map gather moves four rows per 65 cycles, an eighth of what
-//               a tile of 128 columns needs)
+// The experts' first product reads its token rows from a copy in permuted order
+// (permute_rows_kernel): the tensor-map gather moves four rows per 65 cycles, an
+// eighth of what a tile of 128 columns needs (2.16 ms against 0.75 for the product
+// of 16384 rows by 32 experts' 4096 x 7168), and 16-byte asynchronous copies by
+// four more warps kept too few bytes in flight (1.67 ms). The copy takes 0.05 ms.
 #pragma once
 
 namespace mhc {
 
 constexpr int kPairTileM = 256;
-constexpr int kPairLag = 2;  // gathered stages in flight behind the one being issued
 
 __device__ __forceinline__ void tmem_alloc2(unsigned* slot, unsigned cols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols)
@@ -65,12 +65,42 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
 __device__ __forceinline__ void mbar_arrive_cluster(unsigned addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
-__device__ __forceinline__ void cp_async16_or_zero(unsigned dst, const void* src, bool has) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(has ? 16 : 0) : "memory");
+// x [x_rows, k] rows in permuted order: out[q] = x[permuted_rows[q]] for the places
+// that an expert owns. A warp copies 4 KB of a row at a time.
+__global__ void __launch_bounds__(256) permute_rows_kernel(const GemmParams p, __nv_bfloat16* out) {
+  griddep_wait();
+  griddep_launch_dependents();
+  bool bad = false;
+  for (int e = threadIdx.x; e < p.experts; e += 256) {
+    const int lo = p.offsets[e], hi = p.offsets[e + 1];
+    bad |= lo < 0 || hi < lo || hi > p.rows;
+  }
+  if (__syncthreads_or(bad)) return;  // nothing is computed; the products record it
+  const int first = p.offsets[0], used = p.offsets[p.experts];
+  const int lane = threadIdx.x & 31;
+  const int units = p.k / 8, pieces = (units + 255) / 256;  // 16-byte units of a row, 256 a piece
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * 8, total = static_cast<int64_t>(used - first) * pieces;
+  for (int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); w < total; w += warps) {
+    const int q = first + static_cast<int>(w / pieces), u0 = static_cast<int>(w % pieces) * 256 + lane;
+    int r = p.prow[q];
+    if (r < 0 || r >= p.x_rows) {
+      record_error(p.status, MHC_ERR_DEVICE_INDEX);
+      r = 0;
+    }
+    const uint4* src = reinterpret_cast<const uint4*>(p.x + r * p.x_stride);
+    uint4* dst = reinterpret_cast<uint4*>(out + static_cast<int64_t>(q) * p.k);
+    uint4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (u0 + 32 * i < units) v[i] = src[u0 + 32 * i];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (u0 + 32 * i < units) dst[u0 + 32 * i] = v[i];
+  }
 }
 
 template <bool GATED, int SRC>
-__global__ void __cluster_dims__(2) __launch_bounds__(SRC == kGather ? 320 : 192, 1)
+__global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1)
     pair_kernel(const __grid_constant__ GemmParams p, const __grid_constant__ CUtensorMap tm_w,
                 const __grid_constant__ CUtensorMap tm_x) {
   extern __shared__ unsigned char raw[];
@@ -91,9 +121,9 @@ __global__ void __cluster_dims__(2) __launch_bounds__(SRC == kGather ? 320 : 192
   }
   if (tid == 0) {
     prefetch_tensormap(&tm_w);
-    if (SRC != kGather) prefetch_tensormap(&tm_x);
+    prefetch_tensormap(&tm_x);
     for (int i = 0; i < p.stages; ++i) {
-      mbar_init(&full[i], SRC == kGather ? 1 + 8 : 1);  // the copies' bytes, and both CTAs' gathering warps
+      mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -109,7 +139,8 @@ __global__ void __cluster_dims__(2) __launch_bounds__(SRC == kGather ? 320 : 192
   if constexpr (SRC == kDense) {
     tiles = p.m_tiles * ((p.rows + p.bn - 1) / p.bn);
   } else {
-    if constexpr (SRC == kGather) griddep_wait();  // as in gemm_kernel
+    // As in gemm_kernel: the kernel before waited for the offsets before it let this
+    // one start.
     if (warp == 0) expert_tiles(p, first, off, lane);
   }
   tcgen05_fence_before();
@@ -127,7 +158,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(SRC == kGather ? 320 : 192
   if (warp == 0) {
     // ------------------------------------------------ copies
     const unsigned bar0 = cluster_address(smem_u32(&full[0]), 0);
-    if constexpr (SRC != kGather) griddep_wait();
+    griddep_wait();
     int s = 0;
     unsigned ph = 1;
     bool ok = true;
@@ -136,7 +167,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(SRC == kGather ? 320 : 192
       const int half = round32(t.ntok) / 2;
       const int wrow = (SRC == kDense ? 0 : t.expert * (kAcc * p.n)) + t.m * kPairTileM + rank * kTileM;
       const int xrow = t.tok0 + rank * half;
-      const unsigned bytes = kAcc * kATile + (SRC == kDense ? x_bytes : SRC == kGrouped ? half * 128 : 0);
+      const unsigned bytes = kAcc * kATile + (SRC == kDense ? x_bytes : half * 128);
       for (int kb = 0; kb < p.kblocks; ++kb) {
         if (!(ok = __all_sync(kFull, wait_for_cluster(&empty[s], ph, p)))) break;
         if (elect_one()) {
@@ -198,9 +229,9 @@ __global__ void __cluster_dims__(2) __launch_bounds__(SRC == kGather ? 320 : 192
         }
       }
     }
-  } else if (warp < 6) {
+  } else {
     // ------------------------------------------------ epilogue
-    if constexpr (SRC != kGather) griddep_wait();
+    griddep_wait();
     const int q = warp & 3;
     int buf = 0;
     unsigned ph = 0;
@@ -228,54 +259,6 @@ __global__ void __cluster_dims__(2) __launch_bounds__(SRC == kGather ? 320 : 192
         ph ^= 1;
       }
     }
-  } else if constexpr (SRC == kGather) {
-    // ------------------------------------------------ gathered token rows
-    const int g = tid - 192, col = g & 7, r0 = g >> 3;  // 16-byte column; rows r0, r0 + 16, ...
-    const unsigned bar0 = cluster_address(smem_u32(&full[0]), 0);
-    const unsigned dst0 = x0 + r0 * 128 + ((col ^ (r0 & 7)) << 4);
-    int s = 0, i = 0, told = 0;  // stage, stages issued, stages reported
-    unsigned ph = 1;
-    bool ok = true;
-    auto report = [&]() {  // the oldest unreported stage has landed
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(bar0 + (told % p.stages) * 8);
-      ++told;
-    };
-    for (int tile = pair; ok && tile < tiles; tile += pairs) {
-      const TileAt t = tile_even<SRC>(p, first, off, tile);
-      const int half = round32(t.ntok) / 2;
-      const __nv_bfloat16* row[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int c = rank * half + r0 + 16 * j;
-        int r = r0 + 16 * j < half && c < t.ntok ? p.prow[t.tok0 + c] : 0;
-        if (r < 0 || r >= p.x_rows) {
-          record_error(p.status, MHC_ERR_DEVICE_INDEX);
-          r = 0;
-        }
-        row[j] = p.x + r * p.x_stride + col * 8;
-      }
-      for (int kb = 0; kb < p.kblocks; ++kb) {
-        if (!(ok = __all_sync(kFull, wait_for_cluster(&empty[s], ph, p)))) break;
-        const unsigned dst = dst0 + s * x_bytes;
-        const bool has = kb * 64 + col * 8 < p.k;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (16 * j < half) cp_async16_or_zero(dst + j * 2048, row[j] + (has ? kb * 64 : 0), has);
-        cp_async_commit();
-        if (++i - told > kPairLag) {
-          asm volatile("cp.async.wait_group %0;" ::"n"(kPairLag) : "memory");
-          report();
-        }
-        if (++s == p.stages) {
-          s = 0;
-          ph ^= 1;
-        }
-      }
-    }
-    cp_async_wait_all();
-    while (told < i) report();
   }
   tcgen05_fence_before();
   __syncthreads();

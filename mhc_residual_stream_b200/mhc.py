@@ -150,9 +150,8 @@ def _p(t: Optional[torch.Tensor]):
 
 
 def _stream(stream) -> int:
-    if stream is None:  # the raw handle of the current stream, without a Stream object (3 us a call)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
-    return stream.cuda_stream
+    s = stream if stream is not None else torch.cuda.current_stream()
+    return s.cuda_stream
 
 
 def _need(t, dtype, name, dims=None):
@@ -505,17 +504,38 @@ def mxfp8_quantize_rows(x, data, scale, swizzled_128x4: bool = True, stream=None
 
 # ------------------------------------------------------------------ sublayer products and routing
 
-def _here(t):
-    """The tensors of a sublayer call lie on the current device, whose stream it runs on."""
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {t.device}, current device cuda:{torch.cuda.current_device()}")
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
-def _with(first, *others):
-    _here(first)
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and {t.device}")
+def _arg(t, dtype, dims, name, dev, contiguous=True):
+    """The address of an argument (None for None) after its checks: a CUDA tensor on
+    device `dev` (the current one, whose stream the call runs on) of the given type
+    and dims. One pass, for calls of a few microseconds."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.dim() != dims or t.get_device() != dev \
+            or (contiguous and not t.is_contiguous()):
+        _need(t, dtype, name, dims)
+        if contiguous:
+            _contig(t, name)
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+    return t.data_ptr()
+
+
+def _device() -> int:
+    """The current device; -2, which no tensor is on, before CUDA is used."""
+    return torch._C._cuda_getDevice() if torch.cuda._initialized else -2
+
+
+def _raw_stream(stream, dev: int) -> int:
+    # without a Stream object, which takes 3 us to make
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _ws(t, dev):
+    if t is None:
+        return None, 0
+    return _arg(t, _U8, 1, "workspace", dev), t.shape[0]
 
 
 def _workspace(n: int, where: str, device):
@@ -526,10 +546,11 @@ def _workspace(n: int, where: str, device):
 
 def _row_stride(t, name):
     """The stride between the rows of a matrix whose rows are contiguous."""
+    rs, cs = t.stride()
     R, C = t.shape
-    if C > 1 and t.stride(1) != 1:
+    if cs != 1 and C > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return t.stride(0) if R > 1 else (C + 15) // 16 * 16
+    return rs if R > 1 else (C + 15) // 16 * 16
 
 
 def mhc_linear_workspace_bytes(rows: int) -> int:
@@ -541,20 +562,22 @@ def new_linear_workspace(rows: int, device=None) -> torch.Tensor:
     return _workspace(mhc_linear_workspace_bytes(rows), "mhc_linear_workspace_bytes", device)
 
 
-def _operand(v, name):
-    """(data, scale) of a bf16 matrix, or of an MXFP8 one given as (data, scale, swizzled)."""
+def _operand(v, name, dev, contiguous):
+    """(data, address, scale address) of a bf16 matrix, or of an MXFP8 one given as
+    (data, scale, swizzled)."""
     if isinstance(v, torch.Tensor):
-        _need(v, torch.bfloat16, name, 2)
-        return v, None
+        return v, _arg(v, _BF16, 2, name, dev, contiguous), None
     data, scale, swizzled = v
-    _need(data, torch.uint8, name + " data", 2)
-    _need(scale, torch.uint8, name + " scale")
-    _contig(scale, name + " scale")
+    pd = _arg(data, _U8, 2, name + " data", dev, contiguous)
+    _need(scale, _U8, name + " scale")
+    ps = _arg(scale, _U8, scale.dim(), name + " scale", dev)
     if not swizzled:
         raise ValueError(f"{name} scales must be in the swizzled 128x4 layout")
-    if data.shape[1] % 32 == 0 and scale.numel() < mhc_mxfp8_scale_bytes(data.shape[0], data.shape[1], True):
-        raise ValueError(f"{name} scale needs {mhc_mxfp8_scale_bytes(data.shape[0], data.shape[1], True)} bytes")
-    return data, scale
+    R, K = data.shape
+    need = (R + 127) // 128 * 128 * ((K + 127) // 128 * 4)
+    if scale.numel() < need:
+        raise ValueError(f"{name} scale needs {need} bytes")
+    return data, pd, ps
 
 
 def mhc_linear(x, weight, out, bias=None, activation: str = "none", residual=None, workspace=None, stream=None):
@@ -562,31 +585,30 @@ def mhc_linear(x, weight, out, bias=None, activation: str = "none", residual=Non
     x and weight are bf16, or both MXFP8 as (data, scale, True); out is bf16 or fp32.
     activation: none, relu, silu, gelu, or swiglu (weight [2N, K], bias [2N]: gate rows,
     then up rows). Rows of x, residual and out may be strided; residual may be out."""
-    if activation not in ACTIVATIONS:
+    act = ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
-    xd, xs = _operand(x, "x")
-    wd, wsc = _operand(weight, "weight")
-    if (xs is None) != (wsc is None):
+    dev = _device()
+    xd, px, pxs = _operand(x, "x", dev, False)
+    wd, pw, pws = _operand(weight, "weight", dev, True)
+    if (pxs is None) != (pws is None):
         raise TypeError("x and weight must both be bf16 or both MXFP8")
-    _contig(wd, "weight")
-    fp32 = isinstance(out, torch.Tensor) and out.dtype == torch.float32
-    _need(out, torch.float32 if fp32 else torch.bfloat16, "out", 2)
-    _need(bias, torch.float32, "bias", 1)
-    _contig(bias, "bias")
-    _need(residual, torch.bfloat16, "residual", 2)
-    _with(xd, xs, wd, wsc, out, bias, residual, workspace)
+    fp32 = isinstance(out, torch.Tensor) and out.dtype is _F32
+    po = _arg(out, _F32 if fp32 else _BF16, 2, "out", dev, False)
+    pb = _arg(bias, _F32, 1, "bias", dev)
+    pr = _arg(residual, _BF16, 2, "residual", dev, False)
+    pws_, wsb = _ws(workspace, dev)
     R, K = xd.shape
-    N = out.shape[1]
-    W = 2 * N if activation == "swiglu" else N
-    if tuple(wd.shape) != (W, K) or out.shape[0] != R or (bias is not None and bias.shape[0] != W) \
-            or (residual is not None and tuple(residual.shape) != (R, N)):
+    ro, N = out.shape
+    W = 2 * N if act == 4 else N
+    if wd.shape != (W, K) or ro != R or (pb is not None and bias.shape[0] != W) \
+            or (pr is not None and residual.shape != (R, N)):
         raise ValueError("x/weight/bias/residual/out shapes disagree")
-    st = lib().mhc_linear(
-        _p(xd), _p(xs), _row_stride(xd, "x"), _p(wd), _p(wsc), _p(bias), ACTIVATIONS[activation], _p(residual),
-        0 if residual is None else _row_stride(residual, "residual"), _p(out), 1 if fp32 else 0,
-        _row_stride(out, "out"), R, K, N, _p(workspace), 0 if workspace is None else workspace.numel(),
-        _stream(stream))
-    _check(st, "mhc_linear")
+    st = (_lib or lib()).mhc_linear(px, pxs, _row_stride(xd, "x"), pw, pws, pb, act, pr,
+                          0 if pr is None else _row_stride(residual, "residual"), po, fp32, _row_stride(out, "out"),
+                          R, K, N, pws_, wsb, _raw_stream(stream, dev))
+    if st:
+        raise MhcError(st, "mhc_linear")
 
 
 def mhc_moe_route_workspace_bytes(rows: int, experts: int, top_k: int) -> int:
@@ -604,35 +626,30 @@ def mhc_moe_route(logits, expert_weights, expert_ids, expanded_idx_to_permuted_i
     """Experts of each row of logits [R, E] (fp32 or bf16) and the permutation of the
     (row, slot) pairs by expert: expert_weights [R, k] fp32, expert_ids [R, k],
     expanded_idx_to_permuted_idx [R*k], permuted_rows [R*k], expert_offsets [E+1] int32."""
-    if scoring not in SCORES:
+    score = SCORES.get(scoring)
+    if score is None:
         raise ValueError(f"scoring must be one of {sorted(SCORES)}")
-    bf16 = isinstance(logits, torch.Tensor) and logits.dtype == torch.bfloat16
-    _need(logits, torch.bfloat16 if bf16 else torch.float32, "logits", 2)
-    _need(bias, torch.float32, "bias", 1)
-    _need(expert_weights, torch.float32, "expert_weights", 2)
-    _need(expert_ids, torch.int32, "expert_ids", 2)
-    for t, n in ((expanded_idx_to_permuted_idx, "expanded_idx_to_permuted_idx"), (permuted_rows, "permuted_rows"),
-                 (expert_offsets, "expert_offsets")):
-        _need(t, torch.int32, n, 1)
-    for t, n in ((logits, "logits"), (bias, "bias"), (expert_weights, "expert_weights"), (expert_ids, "expert_ids"),
-                 (expanded_idx_to_permuted_idx, "expanded_idx_to_permuted_idx"), (permuted_rows, "permuted_rows"),
-                 (expert_offsets, "expert_offsets")):
-        _contig(t, n)
-    _with(logits, bias, expert_weights, expert_ids, expanded_idx_to_permuted_idx, permuted_rows, expert_offsets,
-          workspace)
+    dev = _device()
+    bf16 = isinstance(logits, torch.Tensor) and logits.dtype is _BF16
+    pl = _arg(logits, _BF16 if bf16 else _F32, 2, "logits", dev)
+    pb = _arg(bias, _F32, 1, "bias", dev)
+    pw = _arg(expert_weights, _F32, 2, "expert_weights", dev)
+    pi = _arg(expert_ids, _I32, 2, "expert_ids", dev)
+    pe = _arg(expanded_idx_to_permuted_idx, _I32, 1, "expanded_idx_to_permuted_idx", dev)
+    pp = _arg(permuted_rows, _I32, 1, "permuted_rows", dev)
+    po = _arg(expert_offsets, _I32, 1, "expert_offsets", dev)
+    pws, wsb = _ws(workspace, dev)
     R, E = logits.shape
-    k = expert_weights.shape[1]
-    if expert_weights.shape[0] != R or tuple(expert_ids.shape) != (R, k) \
-            or expanded_idx_to_permuted_idx.shape[0] != R * k or permuted_rows.shape[0] != R * k \
-            or expert_offsets.shape[0] != E + 1 or (bias is not None and bias.shape[0] != E):
+    rw, k = expert_weights.shape
+    if rw != R or expert_ids.shape != (R, k) or expanded_idx_to_permuted_idx.shape[0] != R * k \
+            or permuted_rows.shape[0] != R * k or expert_offsets.shape[0] != E + 1 \
+            or (pb is not None and bias.shape[0] != E):
         raise ValueError("MoE route shapes disagree")
-    a = RouteArgs(SCORES[scoring], int(num_groups), int(top_groups), int(group_top), k, 1 if renormalize else 0,
-                  float(weight_scale))
-    st = lib().mhc_moe_route(
-        _p(logits), 1 if bf16 else 0, _p(bias), ctypes.byref(a), _p(expert_weights), _p(expert_ids),
-        _p(expanded_idx_to_permuted_idx), _p(permuted_rows), _p(expert_offsets), R, E, _p(workspace),
-        0 if workspace is None else workspace.numel(), _stream(stream))
-    _check(st, "mhc_moe_route")
+    a = RouteArgs(score, num_groups, top_groups, group_top, k, renormalize, weight_scale)
+    st = (_lib or lib()).mhc_moe_route(pl, bf16, pb, ctypes.byref(a), pw, pi, pe, pp, po, R, E, pws, wsb,
+                             _raw_stream(stream, dev))
+    if st:
+        raise MhcError(st, "mhc_moe_route")
 
 
 def mhc_moe_experts_workspace_bytes(rows: int, num_permuted: int, intermediate: int) -> int:
@@ -648,25 +665,23 @@ def new_moe_experts_workspace(rows: int, num_permuted: int, intermediate: int, d
 def mhc_moe_experts(x, w13, w2, permuted_rows, expert_offsets, gemm2_permuted, workspace=None, stream=None):
     """gemm2_permuted [P, H] of the permuted rows: w2[e] (silu(gate) * up) with gate and up
     from w13[e] [2I, H] and the rows x[permuted_rows], expert by expert (expert_offsets)."""
-    _need(x, torch.bfloat16, "x", 2)
-    _need(w13, torch.bfloat16, "w13", 3)
-    _need(w2, torch.bfloat16, "w2", 3)
-    _need(permuted_rows, torch.int32, "permuted_rows", 1)
-    _need(expert_offsets, torch.int32, "expert_offsets", 1)
-    _need(gemm2_permuted, torch.bfloat16, "gemm2_permuted", 2)
-    for t, n in ((w13, "w13"), (w2, "w2"), (permuted_rows, "permuted_rows"), (expert_offsets, "expert_offsets"),
-                 (gemm2_permuted, "gemm2_permuted")):
-        _contig(t, n)
-    _with(x, w13, w2, permuted_rows, expert_offsets, gemm2_permuted, workspace)
+    dev = _device()
+    px = _arg(x, _BF16, 2, "x", dev, False)
+    p13 = _arg(w13, _BF16, 3, "w13", dev)
+    p2 = _arg(w2, _BF16, 3, "w2", dev)
+    pp = _arg(permuted_rows, _I32, 1, "permuted_rows", dev)
+    po = _arg(expert_offsets, _I32, 1, "expert_offsets", dev)
+    pg = _arg(gemm2_permuted, _BF16, 2, "gemm2_permuted", dev)
+    pws, wsb = _ws(workspace, dev)
     R, H = x.shape
-    E, I, P = w2.shape[0], w2.shape[2], permuted_rows.shape[0]
-    if tuple(w13.shape) != (E, 2 * I, H) or w2.shape[1] != H or expert_offsets.shape[0] != E + 1 \
-            or tuple(gemm2_permuted.shape) != (P, H):
+    E, h2, I = w2.shape
+    P = permuted_rows.shape[0]
+    if w13.shape != (E, 2 * I, H) or h2 != H or expert_offsets.shape[0] != E + 1 or gemm2_permuted.shape != (P, H):
         raise ValueError("MoE experts shapes disagree")
-    st = lib().mhc_moe_experts(
-        _p(x), _row_stride(x, "x"), _p(w13), _p(w2), _p(permuted_rows), _p(expert_offsets), _p(gemm2_permuted), R, P,
-        E, H, I, _p(workspace), 0 if workspace is None else workspace.numel(), _stream(stream))
-    _check(st, "mhc_moe_experts")
+    st = (_lib or lib()).mhc_moe_experts(px, _row_stride(x, "x"), p13, p2, pp, po, pg, R, P, E, H, I, pws, wsb,
+                               _raw_stream(stream, dev))
+    if st:
+        raise MhcError(st, "mhc_moe_experts")
 
 
 def mhc_status_string(status: int) -> str:
