@@ -32,7 +32,7 @@
  *     kernel launched immediately before on the same stream if that kernel
  *     triggers dependent launches (no kernel of this library writes weights;
  *     kernels that do not trigger, like ordinary library kernels, are waited
- *     for in full). Activations are read only after the wait.
+ *     for in full; mxfp8_quantize_rows does not trigger). Activations are read only after the wait.
  *   - Errors are returned, never raised or aborted on. Errors found by a kernel
  *     (a wait that ran out, a gather index out of range) are recorded in the
  *     workspace and read with mhc_get_device_status.
@@ -327,9 +327,11 @@ MHC_API mhc_status mxfp8_quantize_rows(const mhc_bf16* x, int rows, int hidden,
  * expanded_idx_to_permuted_idx and gemm2_permuted ([decode] SpecializedDecode.run:
  * MoEStep; the pages name these steps and print none of their arithmetic).
  * Rows are tokens; 1 <= rows <= 65535 here (a prompt's rows too, not only a
- * decode batch's). The conventions above hold, with the dependent-launch rule for
- * weights read as: mhc_linear requests `weight` and `weight_scale` before it waits
- * for the kernel before it on the stream.
+ * decode batch's). The conventions above hold. Their rule on weights and dependent
+ * launches concerns `weight` and `weight_scale` of mhc_linear, which it reads ahead
+ * of its wait: they must not be an output of the mhc_linear, mhc_moe_experts or
+ * boundary call launched directly before on the stream (mxfp8_quantize_rows,
+ * mhc_projection_pack and kernels of other libraries may write them there).
  *
  * mhc_linear: out[r, f] = act( sum_k x[r, k] weight[f, k] + bias[f] ) + residual[r, f]
  *   x [rows, in] and weight [out, in] (contiguous) are bf16 (both scales NULL), or

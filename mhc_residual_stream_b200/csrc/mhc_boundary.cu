@@ -1182,8 +1182,9 @@ __global__ void __launch_bounds__(256) pack_projection_kernel(const float* __res
 __global__ void __launch_bounds__(256) mxfp8_rows_kernel(const __nv_bfloat16* __restrict__ x, int R, int H,
                                                           uint8_t* __restrict__ data, uint8_t* __restrict__ scale,
                                                           int swizzled) {
+  // No early launch of the next kernel: what is quantized here may be the weight that
+  // a following mhc_linear reads ahead of its wait.
   griddep_wait();
-  griddep_launch_dependents();
   const int lanes_per_row = H / 8;
   const int scols = H / 32;
   const int col_tiles = (scols + 3) / 4;
@@ -1236,7 +1237,6 @@ __global__ void __launch_bounds__(256) mxfp8_rows_kernel(const __nv_bfloat16* __
 // Zero the padding bytes of a swizzled scale buffer (rows >= R or columns >= H/32).
 __global__ void scale_padding_kernel(uint8_t* scale, int R, int H) {
   griddep_wait();
-  griddep_launch_dependents();
   const int scols = H / 32;
   const int col_tiles = (scols + 3) / 4;
   const int rows_p = (R + 127) & ~127;

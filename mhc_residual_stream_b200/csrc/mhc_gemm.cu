@@ -522,7 +522,9 @@ __global__ void __launch_bounds__(kGemmThreads, CTAS)
     __syncwarp();
     cluster_arrive();  // this CTA runs and its barriers are set
   }
-  griddep_launch_dependents();
+  // The next kernel may start once this one has itself waited for the one before: what
+  // it reads ahead of its own wait is then older than its direct predecessor.
+  if constexpr (SRC == kGather) griddep_launch_dependents();
   if constexpr (SRC != kDense) tiles = first[p.experts];
   const unsigned tmem = tmem_slot;
   const Schedule sched = clustered ? Schedule(p.kblocks, p.max_split) : Schedule(tiles, p.kblocks, p.max_split, 0);
@@ -558,6 +560,7 @@ __global__ void __launch_bounds__(kGemmThreads, CTAS)
       }
       __syncwarp();
       griddep_wait();
+      griddep_launch_dependents();
     }
     Segments it(sched);
     Segment g;

@@ -147,7 +147,6 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1)
   __syncthreads();
   tcgen05_fence_after();
   cluster_arrive();
-  griddep_launch_dependents();
   if constexpr (SRC != kDense) tiles = first[p.experts];
   const unsigned tmem = tmem_slot;
   cluster_wait();  // the other CTA's barriers are set
@@ -159,6 +158,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1)
     // ------------------------------------------------ copies
     const unsigned bar0 = cluster_address(smem_u32(&full[0]), 0);
     griddep_wait();
+    griddep_launch_dependents();
     int s = 0;
     unsigned ph = 1;
     bool ok = true;

@@ -533,8 +533,8 @@ __global__ void __launch_bounds__(kManyWarps * 32) place_kernel(const RouteParam
 template <typename T, int V>
 __global__ void __launch_bounds__(kFewWarps * 32) route_kernel(const RouteParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
-  griddep_launch_dependents();
   choose_rows<T, V, kFewWarps>(p, smem);
+  griddep_launch_dependents();
   __threadfence();
   __syncthreads();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");

@@ -2,7 +2,7 @@
 
 Mirrors the layer loop of vllm ...specialized_decode.runtime.decode,
 SpecializedDecode.run, with the sublayers (attention, MoE) replaced by seeded
-synthetic outputs: per layer the attention entry (the first layer's broadcast,
+synthetic outputs (with `moe` set, the MoE sublayers run: moe.py): per layer the attention entry (the first layer's broadcast,
 else the finalize of the previous MoE output with an MXFP8 layer input), the
 attention's TP-partial output, the FFN entry (the partial sum, bf16 layer
 input) and the MoE's unfinalized output; after the last layer the finalize
@@ -26,6 +26,7 @@ import torch
 
 from . import mhc as M
 from . import synthetic as S
+from .moe import MoeConfig, MoeSublayer, MoeWeights
 
 
 @dataclass
@@ -48,13 +49,14 @@ class Pending:
 @dataclass
 class Step:
     """One boundary of the schedule."""
-    kind: str            # "first", "attn", "ffn", "post_only", "engram", "final"
+    kind: str            # "first", "attn", "ffn", "post_only", "engram", "final"; "moe" is a sublayer, no boundary
     layer: int
     weights: Optional[BoundaryWeights]
     pending: Optional[Pending]
     mxfp8: bool
     src: int = 0         # state slot read
     dst: int = 0         # state slot written
+    moe: Optional[MoeWeights] = None
 
 
 @dataclass
@@ -75,6 +77,9 @@ class DecodeLoop:
     # SpecializedDecode.run: post_only, the injection, then Boundaries.pre on
     # the injected streams); the injection is a seeded delta (it needs weights)
     engram_layers: Tuple[int, ...] = ()
+    # MoE sublayers computed from the layer input, with seeded weights of their own
+    # per layer, in place of seeded outputs (top_k is then the config's)
+    moe: Optional[MoeConfig] = None
     steps: List[Step] = field(default_factory=list)
 
     def __post_init__(self):
@@ -122,6 +127,10 @@ class DecodeLoop:
             g = S.gen(seed)
             return Pending("engram", delta=(torch.randn(R, n, H, generator=g) * 0.05).to(torch.bfloat16).to(dev))
 
+        self.moe_sublayer = None
+        if self.moe is not None:
+            self.top_k = self.moe.top_k
+            self.moe_sublayer = MoeSublayer(self.moe, R, H, dev)
         steps = []
         slot = 0
         prev_moe = None
@@ -141,7 +150,14 @@ class DecodeLoop:
             attn_out = attn_pending(base + 2)
             steps.append(Step("ffn", layer, weights(base + 3), attn_out, False, src=slot, dst=1 - slot))
             slot = 1 - slot
-            prev_moe = moe_pending(base + 4)
+            if self.moe_sublayer is None:
+                prev_moe = moe_pending(base + 4)
+            else:
+                m = self.moe_sublayer
+                steps.append(Step("moe", layer, None, None, False, src=slot, dst=slot,
+                                  moe=MoeWeights.draw(self.moe, H, base + 4, dev)))
+                prev_moe = Pending("moe", gemm2_permuted=m.gemm2_permuted, expert_weights=m.expert_weights, e2p=m.e2p,
+                                   shared_output=m.shared_output)
         steps.append(Step("final", self.layers, None, prev_moe, False, src=slot, dst=1 - slot))
         self.steps = steps
         self.final_slot = 1 - slot
@@ -154,6 +170,9 @@ class DecodeLoop:
             M.mhc_coeffs(st.weights.coeffs, self.post[st.dst], self.comb[st.dst], self.pre[st.dst], x=self.x,
                          residual_out=self.res[st.dst], norm_weight=st.weights.norm_weight, norm_eps=1e-6,
                          layer_input=self.layer_input, workspace=ws, stream=stream)
+            return
+        if st.kind == "moe":
+            self.moe_sublayer.run(self.layer_input, st.moe, stream)
             return
         a, b = st.src, st.dst
         aux = self.aux_of(st)
@@ -211,7 +230,8 @@ class DecodeLoop:
         return self.res[self.final_slot]
 
     def algorithmic_bytes(self) -> int:
-        """Bytes each boundary must move (inputs read once, outputs written once), summed."""
+        """Bytes each boundary must move (inputs read once, outputs written once), summed;
+        the MoE sublayers' own are not counted."""
         R, H, n = self.rows, self.hidden, self.hc_mult
         C = 2 * n + n * n
         total = 0
@@ -220,6 +240,8 @@ class DecodeLoop:
             fn_b = n * H * C * 4 + (3 + C) * 4
             mix_in = R * (2 * n + n * n) * 4
             coeff_out = R * (2 * n + n * n) * 4
+            if st.kind == "moe":
+                continue
             if st.kind == "first":
                 b = R * H * 2 + R * n * H * 2 + R * H * 2 + fn_b + H * 2 + coeff_out
             elif st.kind == "engram":  # the injection's add is the stand-in's, not counted
