@@ -65,6 +65,7 @@ struct GemmParams {
   int n;         // output features
   int kblocks;   // K in blocks of 128 bytes
   int m_tiles, bn, stages, nbuf, tmem_cols, experts;
+  int apart;      // a cluster's sums have shared memory of their own, beside the ring
   int max_split;  // grouped: CTAs that may share a tile; dense: CTAs of a cluster, all on one tile
   unsigned idesc;
   const int32_t* offsets;  // [experts + 1]
@@ -278,6 +279,14 @@ __device__ __forceinline__ bool epilogue_all(bool ok) {
 // the wait. Whole warps.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// Of the warps that have no part in a cluster's epilogue: its two barriers but the
+// second one's wait, which ends the kernel.
+__device__ __forceinline__ void pass_cluster_barriers(bool apart) {
+  __syncwarp();
+  if (!apart) cluster_arrive();
+  cluster_wait();
+  cluster_arrive();
+}
 __device__ __forceinline__ unsigned cluster_address(unsigned addr, int rank) {
   unsigned r;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
@@ -383,14 +392,15 @@ __device__ __forceinline__ void add4(float (&v)[4], const float4 a) {
 }
 
 // The epilogue of a tile that a cluster computes, K divided over its CTAs: token
-// column c is finished by CTA c / each. A CTA lays its sums out by that CTA in its
-// drained ring, [CTA][gate, up][column / 4][feature][4], and one bulk copy per CTA
-// takes them there; the columns that arrive are added in CTA order, which is K
-// order. (Threads storing the sums remotely took 120 cycles per 512 bytes.)
+// column c is finished by CTA c / each. A CTA lays its sums out by that CTA in the
+// first part of its drained ring, [CTA][gate, up][column / 4][feature][4], and one
+// bulk copy per CTA takes them to that CTA: to memory of their own beside the ring, or
+// to the second part of its ring once all rings are drained; the columns that arrive
+// are added in CTA order, which is K order.
 template <bool GATED>
 __device__ __forceinline__ void finish_in_cluster(const GemmParams& p, const Schedule& sched, unsigned char* raw,
-                                                  unsigned smem0, unsigned sums0, unsigned tmem, uint64_t* acc_full,
-                                                  uint64_t* sums_in, int q, int lane) {
+                                                  unsigned smem0, unsigned tmem, unsigned ring_bytes,
+                                                  uint64_t* acc_full, uint64_t* sums_in, int q, int lane) {
   constexpr int kAcc = GATED ? 2 : 1;
   const int S = p.max_split, r = sched.cta % S;
   const TileAt t = tile_at<kDense>(p, nullptr, nullptr, sched.cta / S);
@@ -398,6 +408,7 @@ __device__ __forceinline__ void finish_in_cluster(const GemmParams& p, const Sch
   const int owners = (t.ntok + each - 1) / each;
   const int row = q * 32 + lane, f = t.m * kTileM + row;
   const unsigned block = kAcc * each * kTileM * 4;  // bytes of the sums for one CTA
+  const unsigned sums0 = smem0 + (p.apart ? ring_bytes : columns_each(p.bn, S) * S * kAcc * kTileM * 4);
   const unsigned peer = min(lane, S - 1);
   const unsigned dst = cluster_address(sums0 + r * block, peer), bar = cluster_address(smem_u32(sums_in), peer);
   float bg = 0.f, bu = 0.f;
@@ -407,6 +418,8 @@ __device__ __forceinline__ void finish_in_cluster(const GemmParams& p, const Sch
   }
   unsigned char* out = raw + (smem0 - smem_u32(raw)) + row * 16;
   const bool ok = epilogue_all(wait_for(&acc_full[0], 0, p));
+  __syncwarp();
+  if (!p.apart) cluster_arrive();  // this CTA's ring is drained
   if (ok) {
     tcgen05_fence_after();
     const unsigned src = tmem + (static_cast<unsigned>(q * 32) << 16);
@@ -431,7 +444,7 @@ __device__ __forceinline__ void finish_in_cluster(const GemmParams& p, const Sch
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     epilogue_barrier();
   }
-  cluster_wait();  // every CTA of the cluster runs and its barriers are set
+  cluster_wait();
   if (ok && q == 2 && lane < owners) bulk_s2cluster(dst, smem0 + lane * block, block, bar);
   __syncwarp();
   if (ok && n > 0 && __all_sync(kFull, wait_for_cluster(sums_in, 0, p))) {
@@ -472,8 +485,6 @@ __global__ void __launch_bounds__(kGemmThreads, CTAS)
   // bn is a multiple of 16 rows, so a stage's token rows start on the 1024-byte
   // boundary that the swizzle pattern repeats at
   const unsigned sf0 = x0 + p.stages * x_bytes;
-  // a cluster's sums of this CTA's columns: [CTA][gate, up][column / 4][feature][4]
-  const unsigned sums0 = sf0 + p.stages * sf_bytes;
   int* first = nullptr;  // grouped: first tile of each expert, and its first permuted row
   int* off = nullptr;
   if constexpr (SRC != kDense) {
@@ -519,8 +530,8 @@ __global__ void __launch_bounds__(kGemmThreads, CTAS)
       const int r = blockIdx.x % p.max_split, each = columns_each(t.ntok, p.max_split);
       mbar_arrive_expect_tx(&sums_in, r * each < t.ntok ? p.max_split * (kAcc * each * kTileM * 4) : 0);
     }
-    __syncwarp();
-    cluster_arrive();  // this CTA runs and its barriers are set
+    __syncwarp();  // the copying warp issues from uniform registers only while it is converged
+    if (p.apart) cluster_arrive();  // this CTA runs and its barriers are set
   }
   // The next kernel may start once this one has itself waited for the one before: what
   // it reads ahead of its own wait is then older than its direct predecessor.
@@ -618,11 +629,8 @@ __global__ void __launch_bounds__(kGemmThreads, CTAS)
         mbar_wait_bounded(&full[q], n & 1u, deadline);
       }
     }
-    if (clustered) {
-      __syncwarp();
-      cluster_wait();
-      cluster_arrive();
-    }
+    __syncwarp();
+    if (clustered) pass_cluster_barriers(p.apart);
   } else if (warp == 1) {
     // ------------------------------------------------ products
     const unsigned a_lo = desc_lo(smem0), b_lo = desc_lo(x0), idesc = p.idesc;
@@ -676,15 +684,13 @@ __global__ void __launch_bounds__(kGemmThreads, CTAS)
       }
     }
     __syncwarp();
-    if (clustered) {
-      cluster_wait();
-      cluster_arrive();
-    }
+    if (clustered) pass_cluster_barriers(p.apart);
   } else {
     // ------------------------------------------------ epilogue
     if constexpr (SRC != kGather) griddep_wait();
     const int q = warp & 3;  // the quarter of the accumulator's lanes this warp can read
-    if (clustered) finish_in_cluster<GATED>(p, sched, raw, smem0, sums0, tmem, acc_full, &sums_in, q, lane);
+    if (clustered) finish_in_cluster<GATED>(p, sched, raw, smem0, tmem, p.stages * (kAcc * kATile + x_bytes + sf_bytes),
+                                             acc_full, &sums_in, q, lane);
     Segments it(sched);
     Segment g;
     int buf = 0;
@@ -814,7 +820,7 @@ bool make_map2(CUtensorMap* m, const void* base, bool bytes, uint64_t cols, uint
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Shared memory of the sums that a cluster's CTAs send one of them.
+// Bytes of a CTA's sums as it lays them out for its cluster, and of those it receives.
 int sums_bytes(int bn, int acc, int split) { return columns_each(bn, split) * split * acc * kTileM * 4; }
 
 // bn, kblocks and the operand types are set: the ring, tensor memory and
@@ -826,10 +832,17 @@ mhc_status launch_gemm(GemmParams& p, const CUtensorMap& w, const CUtensorMap& x
   const int fixed = 1024 + (SRC == kDense ? 0 : 8 * (p.experts + 1));
   const int stage = acc * kATile + p.bn * 128 + (FP8 ? (acc + 1) * 512 : 0);
   const int limit = CTAS == 2 ? kHalfSmem : kGemmSmem - kStaticSmem;
+  // A cluster's sums: apart from the ring where one CTA has the SM's memory (0.25 us
+  // less than in the drained ring, which takes a barrier more on the way), in the ring
+  // where two share it (three stages of 36 KB against two: 160 gated rows 17.4 us
+  // against 18.6).
   const int sums = cluster > 1 ? sums_bytes(p.bn, acc, cluster) : 0;
-  p.stages = (limit - fixed - sums) / stage;
+  p.apart = CTAS == 1;
+  const int beside = p.apart ? sums : 0;
+  p.stages = (limit - fixed - beside) / stage;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
-  const int smem = fixed + p.stages * stage + sums;
+  const int smem = fixed + p.stages * stage + beside;
+  if (p.stages * stage < (p.apart ? 1 : 2) * sums) return MHC_ERR_UNSUPPORTED_SHAPE;
   auto cols = [&](int nbuf) { return nbuf * acc * p.bn + (FP8 ? p.stages * (acc + 1) * 4 : 0); };
   p.nbuf = cluster == 1 && cols(2) <= 512 / CTAS ? 2 : 1;
   p.tmem_cols = 32;
@@ -845,8 +858,7 @@ mhc_status launch_gemm(GemmParams& p, const CUtensorMap& w, const CUtensorMap& x
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MHC_ERR_CUDA;
   if (configured[dev].load(std::memory_order_acquire) == 0) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem - kStaticSmem) !=
-            cudaSuccess ||
-        (SRC == kDense && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)) {
+            cudaSuccess) {
       (void)cudaGetLastError();
       return MHC_ERR_CUDA;
     }
@@ -884,27 +896,24 @@ struct Plan {
   bool pair;
 };
 
-// CTAs that are resident at once in clusters of 1..16, at one and two CTAs an SM,
-// as cudaOccupancyMaxActiveClusters counts them on a B200 (148 SMs in clusters of
-// SMs that larger clusters do not fill).
-constexpr int kRoom[2][16] = {{148, 148, 135, 132, 130, 132, 105, 120, 108, 110, 99, 84, 91, 98, 105, 112},
-                              {296, 296, 279, 284, 280, 270, 259, 264, 243, 260, 253, 252, 234, 224, 210, 224}};
+// CTAs that are resident at once in clusters of 1..8, at one and two CTAs an SM, as
+// cudaOccupancyMaxActiveClusters counts them on a B200 (148 SMs in clusters of SMs
+// that larger clusters do not fill).
+constexpr int kRoom[2][8] = {{148, 148, 135, 132, 130, 132, 105, 120}, {296, 296, 279, 284, 280, 270, 259, 264}};
 
 // Token columns of a tile and CTAs per tile of a dense product: the least of an
 // estimate of the time, in SM cycles, over a few candidates. Its constants fit the
-// times of 27 products (1-2048 rows, K 512-7168, 128-16000 features, plain, gated
-// and MXFP8) with every candidate; the candidate it picks takes 1.9% more than the
-// best one on average, 19% more at worst. A K block costs the largest of
+// times of 32 products (1-2048 rows, K 512-7168, 128-16000 features, plain, gated
+// and MXFP8) with every candidate; the candidate it picks takes 2.3% more than the
+// best one on average, 14% more at worst. A K block costs the largest of
 //   its products, 128 x bn x 64 multiply-adds at 4096 a cycle;
 //   kIssue, the least a K block takes on one SM (its copies, waits and issue);
 //   its copies: what the ring holds per kLatency, at most kCopyRate bytes a cycle on
 //   an SM and kL2Rate over all of them.
-// A tile adds kEpilogue cycles a column, shared by a cluster kJoin + kJoinColumn a
-// column. A pair of CTAs (mhc_pair.cuh) halves the token rows that each copies.
+// A tile adds kEpilogue cycles a column, one shared by a cluster kJoinColumn. A pair of CTAs (mhc_pair.cuh) halves the token rows that each copies.
 Plan plan_linear(const GemmParams& p, int rows, bool fp8, bool gated) {
-  constexpr double kLatency = 2300, kCopyRate = 66, kL2Rate = 7700, kIssue = 510, kEpilogue = 19, kJoin = 630,
-                   kJoinColumn = 125;
-  constexpr int kSplits[] = {1, 2, 3, 4, 5, 6, 8, 12, 16};
+  constexpr double kLatency = 3000, kCopyRate = 45, kL2Rate = 8600, kIssue = 600, kEpilogue = 5, kJoinColumn = 160;
+  constexpr int kSplits[] = {1, 2, 3, 4, 5, 6, 8};
   const int sms = gemm_grid();
   const int acc = gated ? 2 : 1;
   const int cap = fp8 || gated ? 128 : 256;
@@ -923,10 +932,10 @@ Plan plan_linear(const GemmParams& p, int rows, bool fp8, bool gated) {
       for (int split : kSplits) {
         if (split > p.kblocks || tiles * split > (split > 1 ? kRoom[per_sm - 1][split - 1] : 1 << 30)) break;
         if (split == 1 && per_sm == 2) continue;
-        const int room = (per_sm == 2 ? kHalfSmem : kGemmSmem - kStaticSmem) - 1024 -
-                         (split > 1 ? sums_bytes(bn, acc, split) : 0);
+        const int sums = split > 1 ? sums_bytes(bn, acc, split) : 0;
+        const int room = per_sm == 2 ? kHalfSmem - 1024 : kGemmSmem - kStaticSmem - 1024 - sums;
         int stages = room / stage < kMaxStages ? room / stage : kMaxStages;
-        if (stages < 2 || cols > 512 / per_sm) continue;
+        if (stages < 2 || cols > 512 / per_sm || stages * stage < per_sm * sums) continue;
         const int ctas = split > 1 ? tiles * split : (tiles < sms ? tiles : sms);
         const int waves = split > 1 ? 1 : (tiles + sms - 1) / sms;
         const int blocks = (p.kblocks + split - 1) / split;
@@ -938,7 +947,7 @@ Plan plan_linear(const GemmParams& p, int rows, bool fp8, bool gated) {
         double block = (2.0 * acc * bn > kIssue ? 2.0 * acc * bn : kIssue) * shared;
         if (block < bytes / rate) block = bytes / rate;
         const double t = waves * blocks * block +
-                         (split > 1 ? kJoin + kJoinColumn * acc * bn : kEpilogue * acc * bn);
+                         (split > 1 ? kJoinColumn : kEpilogue) * acc * bn;
         if (best.bn == 0 || t < least) {
           least = t;
           best = Plan{bn, split, per_sm, ctas, false};
@@ -949,7 +958,7 @@ Plan plan_linear(const GemmParams& p, int rows, bool fp8, bool gated) {
   if (!fp8 && rows > 64) {
     const int bn = rows < 256 ? round32(rows) : 256;
     const int waves = ((p.n + kPairTileM - 1) / kPairTileM * ((rows + bn - 1) / bn) + sms / 2 - 1) / (sms / 2);
-    const double copies = (acc * kATile + bn / 2 * 128) / (kL2Rate / sms), products = 2.0 * acc * bn;
+    const double copies = (acc * kATile + bn / 2 * 128) / kCopyRate, products = 2.0 * acc * bn;
     double block = copies > products ? copies : products;
     if (block < kIssue) block = kIssue;
     if (waves * p.kblocks * block + kEpilogue * acc * bn < least) best = Plan{bn, 1, 1, sms / 2 * 2, true};
