@@ -262,15 +262,16 @@ __device__ __forceinline__ bool wait_for_cluster(uint64_t* bar, unsigned parity,
 }
 
 __device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-// The same barrier, true where `ok` holds in every epilogue thread: the four warps
-// leave their loop together or not at all.
+// The same barrier, true where `ok` holds in every epilogue thread: its warps leave
+// their loop together or not at all.
+template <int kThreads = 128>
 __device__ __forceinline__ bool epilogue_all(bool ok) {
   unsigned r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "barrier.cta.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(ok ? 1u : 0u)
+      : "r"(ok ? 1u : 0u), "n"(kThreads)
       : "memory");
   return r != 0;
 }
@@ -910,7 +911,8 @@ constexpr int kRoom[2][8] = {{148, 148, 135, 132, 130, 132, 105, 120}, {296, 296
 //   kIssue, the least a K block takes on one SM (its copies, waits and issue);
 //   its copies: what the ring holds per kLatency, at most kCopyRate bytes a cycle on
 //   an SM and kL2Rate over all of them.
-// A tile adds kEpilogue cycles a column, one shared by a cluster kJoinColumn. A pair of CTAs (mhc_pair.cuh) halves the token rows that each copies.
+// A tile adds kEpilogue cycles a column, one shared by a cluster kJoinColumn. A pair
+// of CTAs (mhc_pair.cuh) halves the token rows that each copies.
 Plan plan_linear(const GemmParams& p, int rows, bool fp8, bool gated) {
   constexpr double kLatency = 3000, kCopyRate = 45, kL2Rate = 8600, kIssue = 600, kEpilogue = 5, kJoinColumn = 160;
   constexpr int kSplits[] = {1, 2, 3, 4, 5, 6, 8};
@@ -999,7 +1001,7 @@ mhc_status launch_pair(GemmParams& p, const CUtensorMap& w, const CUtensorMap& x
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(gemm_grid() / 2 * 2);
-  cfg.blockDim = dim3(kGemmThreads);
+  cfg.blockDim = dim3(kPairThreads);
   cfg.dynamicSmemBytes = fixed + p.stages * stage;
   cfg.stream = stream;
   cfg.attrs = attr;

@@ -12,7 +12,8 @@
 //
 //   warp 0      each CTA: copies by tensor map, counted on the first CTA's barrier
 //   warp 1      first CTA: issues the products for both
-//   warps 2-5   each CTA: epilogue of its 128 weight rows
+//   warps 2-9   each CTA: epilogue of its 128 weight rows, two warps to a quarter of them
+//               (a gated tile of 256 columns fills tensor memory, so nothing hides it)
 // The experts' first product reads its token rows from a copy in permuted order
 // (permute_rows_kernel): the tensor-map gather moves four rows per 65 cycles, an
 // eighth of what a tile of 128 columns needs (2.16 ms against 0.75 for the product
@@ -23,6 +24,8 @@
 namespace mhc {
 
 constexpr int kPairTileM = 256;
+constexpr int kPairWarps = 8;  // of the epilogue
+constexpr int kPairThreads = 64 + 32 * kPairWarps;
 
 __device__ __forceinline__ void tmem_alloc2(unsigned* slot, unsigned cols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols)
@@ -100,7 +103,7 @@ __global__ void __launch_bounds__(256) permute_rows_kernel(const GemmParams p, _
 }
 
 template <bool GATED, int SRC>
-__global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1)
+__global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
     pair_kernel(const __grid_constant__ GemmParams p, const __grid_constant__ CUtensorMap tm_w,
                 const __grid_constant__ CUtensorMap tm_x) {
   extern __shared__ unsigned char raw[];
@@ -128,7 +131,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 8);  // both CTAs' epilogue warps
+      mbar_init(&acc_empty[i], 2 * kPairWarps);  // both CTAs' epilogue warps
     }
   }
   if (warp == 1) {
@@ -232,7 +235,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1)
   } else {
     // ------------------------------------------------ epilogue
     griddep_wait();
-    const int q = warp & 3;
+    const int q = warp & 3, part = (warp - 2) >> 2;
     int buf = 0;
     unsigned ph = 0;
     for (int tile = pair; tile < tiles; tile += pairs) {
@@ -243,10 +246,10 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1)
         bg = p.bias[f];
         if constexpr (GATED) bu = p.bias[p.n + f];
       }
-      if (!epilogue_all(wait_for_cluster(&acc_full[buf], ph, p))) break;
+      if (!epilogue_all<32 * kPairWarps>(wait_for_cluster(&acc_full[buf], ph, p))) break;
       tcgen05_fence_after();
       const unsigned src = tmem + buf * acc_cols + (static_cast<unsigned>(q * 32) << 16);
-      for (int c = 0; c < t.ntok; c += 16) {
+      for (int c = 16 * part; c < t.ntok; c += 32) {
         float v[16], u[16];
         read_sums<GATED>(src + c, p.bn, v, u);
         store_columns<GATED, 16>(p, v, u, bg, bu, t.tok0 + c, f, t.ntok - c);
