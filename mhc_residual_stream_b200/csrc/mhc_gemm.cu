@@ -14,17 +14,17 @@
 //              tiles are copied to tensor memory beside them);
 //   warps 2-5  read a finished accumulator (a thread owns one output feature)
 //              and write act(acc + bias) + residual.
-// Dividing the work. A product of at least a tile per SM gives whole tiles to
-// its persistent CTAs. A dense product of fewer divides each tile's K over a
-// cluster of up to 8 CTAs, which add their accumulators through distributed
-// shared memory, each its share of the token columns. The experts' products,
-// whose tiles only the device knows, divide the tiles that are left after the
-// full waves evenly over all CTAs along the flattened (tile, K) axis when a tile
-// has few token columns; a tile shared by several CTAs is joined by whichever of
-// them finishes last: all write their fp32 sums to the workspace and count up,
-// the last adds them and runs the epilogue. Sums are added in K order in every
-// form, so results do not depend on timing, and no CTA waits for another outside
-// its own cluster.
+// Dividing the work. A product of at least a tile per SM gives whole tiles to its
+// persistent CTAs. A dense product of fewer divides each tile's K over a cluster of up
+// to 8 CTAs: each sends its sums of every token column to the CTA of the cluster that
+// finishes the column, through distributed shared memory. The experts' products, whose
+// tiles only the device knows, divide the tiles that are left after the full waves
+// evenly over all CTAs along the flattened (tile, K) axis; a tile shared by several
+// CTAs is joined by whichever of them finishes last: all write their fp32 sums to the
+// workspace and count up, the last adds them and runs the epilogue. Sums are added in
+// K order in every form, so results do not depend on timing, and no CTA waits for
+// another outside its own cluster. Many token rows go to the pair kernel
+// (mhc_pair.cuh), two CTAs on one tile.
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(kGemmThreads, CTAS)
   extern __shared__ unsigned char raw[];
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], sums_in;
   __shared__ unsigned tmem_slot, join_slot;
-  __shared__ __align__(16) int rows[SRC == kGather ? 128 : 4];  // gathered token rows of the tile being copied
+  __shared__ __align__(16) int rows[SRC == kGather ? 32 : 4];  // gathered token rows of the tile being copied
   constexpr int kAcc = GATED ? 2 : 1;
   constexpr int kElems = FP8 ? 128 : 64;  // K elements of a stage's 128-byte rows
   const int tid = threadIdx.x, lane = tid & 31;
@@ -802,7 +802,7 @@ using namespace mhc;
 constexpr int kMaxTokens = 65535;
 constexpr int kMaxK = 65536;
 constexpr int kMaxFeatures = 1 << 20;
-constexpr int kSplitCols = 32;  // most token columns of a tile that several CTAs may share
+constexpr int kSplitCols = 32;  // most token columns of a grouped tile, which several CTAs may share
 
 // Partial sums of the experts' shared tiles: two per CTA, gate and up.
 constexpr size_t kPartialBytes = static_cast<size_t>(kMaxGrid) * 2 * kTileM * 2 * kSplitCols * 4;
@@ -968,9 +968,6 @@ Plan plan_linear(const GemmParams& p, int rows, bool fp8, bool gated) {
   return best;
 }
 
-// Whether the experts' products take the pair kernel: rows of an expert, on average.
-constexpr int kPairMean = 96;
-
 template <bool GATED, int SRC>
 mhc_status launch_pair(GemmParams& p, const CUtensorMap& w, const CUtensorMap& x, cudaStream_t stream) {
   constexpr int acc = GATED ? 2 : 1;
@@ -1114,19 +1111,22 @@ mhc_status mhc_moe_experts(const mhc_bf16* x, int64_t x_stride, const mhc_bf16* 
   p.status = reinterpret_cast<unsigned*>(ws);
   p.counters = reinterpret_cast<unsigned*>(ws + kGemmCounters);
   p.partials = reinterpret_cast<float*>(ws + kGemmHeader);
-  // Token columns of a tile: about twice the mean number of an expert's rows
-  // (its tokens then mostly fit one tile, which reads the weights once), never
-  // more than there are rows.
-  const int mean = (num_permuted + experts - 1) / experts;
-  int bn = mean <= 4 ? 16 : mean <= 16 ? 32 : mean <= 48 ? 64 : 128;
-  if (bn > round16(rows)) bn = round16(rows);
-  const bool pair = mean > kPairMean;
-  if (pair) bn = 256;
+  // By the mean number of an expert's rows. From 12, or from 8 where the weights make
+  // two waves of pair tiles, the pair kernel, whose tile takes up to 256 rows of an
+  // expert (B200, us against tiles of 16-128 rows gathered by tensor map, best of
+  // them; E x 7168 x 2048 unless given): mean 8 786 / 803, 16 816 / 841, 48 865 / 1018,
+  // 64 891 / 1185, 50 (8 experts, 4096 x 1024) 57 / 69; mean 8 (24 experts, 4096 x
+  // 1024, 1.3 waves) 114 / 103, mean 4 245 / 227. Below, tiles of 16 or 32 rows: 18.5
+  // against 20.5 at a mean of 4.6, equal at 8.
+  const int mean = num_permuted / experts;
+  const bool pair = mean >= 12 || (mean >= 8 && static_cast<int64_t>(experts) * ((intermediate + 255) / 256) >=
+                                                    gemm_grid());
+  const int bn = pair ? 256 : mean < 6 || rows <= 16 ? 16 : 32;
   p.bn = bn;
   p.k = hidden;
   p.x = reinterpret_cast<const __nv_bfloat16*>(x);
   p.x_stride = x_stride;
-  p.max_split = bn <= kSplitCols ? kMaxShares - 1 : 1;
+  p.max_split = kMaxShares - 1;
   const int grid = gemm_grid();
   CUtensorMap mw, mx;
   // first product: gate and up rows of an expert's w13, token rows gathered
