@@ -821,6 +821,17 @@ bool make_map2(CUtensorMap* m, const void* base, bool bytes, uint64_t cols, uint
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Scale tiles of 512 bytes (128 words), one a row; rows behind the last read as zero.
+bool make_scale_map(CUtensorMap* m, const void* base, uint64_t tiles) {
+  EncodeTiledFn enc = encode_tiled();
+  if (enc == nullptr) return false;
+  cuuint64_t d[2] = {128, tiles}, st[1] = {512};
+  cuuint32_t b[2] = {128, 1}, e[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), d, st, b, e, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Bytes of a CTA's sums as it lays them out for its cluster, and of those it receives.
 int sums_bytes(int bn, int acc, int split) { return columns_each(bn, split) * split * acc * kTileM * 4; }
 
@@ -957,8 +968,8 @@ Plan plan_linear(const GemmParams& p, int rows, bool fp8, bool gated) {
       }
     }
   }
-  if (!fp8 && rows > 64) {
-    const int bn = rows < 256 ? round32(rows) : 256;
+  if (fp8 ? !gated && rows > 128 : rows > 64) {
+    const int bn = rows < 256 && !fp8 ? round32(rows) : 256;  // MXFP8: tiles start at a scale tile's first row
     const int waves = ((p.n + kPairTileM - 1) / kPairTileM * ((rows + bn - 1) / bn) + sms / 2 - 1) / (sms / 2);
     const double copies = (acc * kATile + bn / 2 * 128) / kCopyRate, products = 2.0 * acc * bn;
     double block = copies > products ? copies : products;
@@ -968,20 +979,22 @@ Plan plan_linear(const GemmParams& p, int rows, bool fp8, bool gated) {
   return best;
 }
 
-template <bool GATED, int SRC>
-mhc_status launch_pair(GemmParams& p, const CUtensorMap& w, const CUtensorMap& x, cudaStream_t stream) {
+template <bool FP8, bool GATED, int SRC>
+mhc_status launch_pair(GemmParams& p, const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& ws,
+                       const CUtensorMap& xs, cudaStream_t stream) {
   constexpr int acc = GATED ? 2 : 1;
   const int fixed = 1024 + (SRC == kDense ? 0 : 8 * (p.experts + 1));
-  const int stage = acc * kATile + p.bn / 2 * 128;
+  const int stage = acc * kATile + p.bn / 2 * 128 + (FP8 ? 3 * 512 : 0);
   p.stages = (kGemmSmem - kStaticSmem - fixed) / stage;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
-  p.nbuf = 2 * acc * p.bn <= 512 ? 2 : 1;
-  if (p.stages < 2 || p.bn % 32 != 0 || acc * p.bn > 512) return MHC_ERR_UNSUPPORTED_SHAPE;
+  const int scale_cols = FP8 ? p.stages * 12 : 0;
+  p.nbuf = 2 * acc * p.bn + scale_cols <= 512 ? 2 : 1;
+  if (p.stages < 2 || p.bn % 32 != 0 || acc * p.bn + scale_cols > 512) return MHC_ERR_UNSUPPORTED_SHAPE;
   p.m_tiles = (p.n + kPairTileM - 1) / kPairTileM;
-  p.idesc = (static_cast<unsigned>(kPairTileM >> 4) << 24) | (1u << 4) | (1u << 7) | (1u << 10);
+  p.idesc = (static_cast<unsigned>(kPairTileM >> 4) << 24) | (FP8 ? 1u << 23 : (1u << 4) | (1u << 7) | (1u << 10));
   p.budget_ns = g_budget_ns;
   p.extra_tx = static_cast<unsigned>(g_extra_tx) * 16;
-  auto kern = pair_kernel<GATED, SRC>;
+  auto kern = pair_kernel<FP8, GATED, SRC>;
   static std::atomic<int> configured[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MHC_ERR_CUDA;
@@ -1003,7 +1016,7 @@ mhc_status launch_pair(GemmParams& p, const CUtensorMap& w, const CUtensorMap& x
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kern, p, w, x) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, kern, p, w, x, ws, xs) != cudaSuccess) {
     (void)cudaGetLastError();
     return MHC_ERR_CUDA;
   }
@@ -1072,7 +1085,15 @@ mhc_status mhc_linear(const void* x, const uint8_t* x_scale, int64_t x_stride, c
   if (!make_map2(&mw, weight, fp8, in_features, wrows, static_cast<uint64_t>(in_features) * row_bytes, kTileM) ||
       !make_map2(&mx, x, fp8, in_features, rows, static_cast<uint64_t>(x_stride) * row_bytes, pair ? p.bn / 2 : p.bn))
     return MHC_ERR_CUDA;
-  if (pair) return gated ? launch_pair<true, kDense>(p, mw, mx, stream) : launch_pair<false, kDense>(p, mw, mx, stream);
+  if (pair && fp8) {
+    CUtensorMap ms, mt;
+    if (!make_scale_map(&ms, weight_scale, (out_features + 127) / 128 * p.kblocks) ||
+        !make_scale_map(&mt, x_scale, (rows + 127) / 128 * p.kblocks))
+      return MHC_ERR_CUDA;
+    return launch_pair<true, false, kDense>(p, mw, mx, ms, mt, stream);
+  }
+  if (pair) return gated ? launch_pair<false, true, kDense>(p, mw, mx, mw, mx, stream)
+                         : launch_pair<false, false, kDense>(p, mw, mx, mw, mx, stream);
   if (fp8) return gated ? launch_linear<true, true>(p, plan, mw, mx, stream)
                         : launch_linear<true, false>(p, plan, mw, mx, stream);
   return gated ? launch_linear<false, true>(p, plan, mw, mx, stream)
@@ -1158,7 +1179,7 @@ mhc_status mhc_moe_experts(const mhc_bf16* x, int64_t x_stride, const mhc_bf16* 
       (void)cudaGetLastError();
       return MHC_ERR_CUDA;
     }
-    st = launch_pair<true, kGrouped>(p, mw, mx, stream);
+    st = launch_pair<false, true, kGrouped>(p, mw, mx, mw, mx, stream);
   } else {
     if (!make_map2(&mx, x, false, hidden, rows, static_cast<uint64_t>(x_stride) * 2, 1)) return MHC_ERR_CUDA;
     st = launch_gemm<false, true, kGather, 1>(p, mw, mx, grid, 1, stream);
@@ -1175,7 +1196,7 @@ mhc_status mhc_moe_experts(const mhc_bf16* x, int64_t x_stride, const mhc_bf16* 
                  static_cast<uint64_t>(intermediate) * 2, kTileM) ||
       !make_map2(&mx, inner, false, intermediate, num_permuted, static_cast<uint64_t>(intermediate) * 2, pair ? 16 : p.bn))
     return MHC_ERR_CUDA;
-  if (pair) return launch_pair<false, kGrouped>(p, mw, mx, stream);
+  if (pair) return launch_pair<false, false, kGrouped>(p, mw, mx, mw, mx, stream);
   return launch_gemm<false, false, kGrouped, 1>(p, mw, mx, grid, 1, stream);
 }
 

@@ -55,6 +55,22 @@ __device__ __forceinline__ void mma_bf16_pair(unsigned d, unsigned a, unsigned b
       "r"(a), "r"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "n"(kDescHi)
       : "memory");
 }
+// The same with E4M3 operands and E8M0 scales (K 32): each CTA's tensor memory holds
+// the scales of its 128 rows of A at sa and of all N rows of B at sb.
+__device__ __forceinline__ void mma_mxf8_pair(unsigned d, unsigned a, unsigned b, unsigned idesc, unsigned sa,
+                                              unsigned sb, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "mov.b64 da, {%1, %7};\n\tmov.b64 db, {%2, %7};\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], da, db, %3, [%5], [%6], p;\n\t}" ::"r"(
+          d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(sa), "r"(sb), "n"(kDescHi)
+      : "memory");
+}
+// tmem_copy_scales in both CTAs, each from its own shared memory at the same address.
+__device__ __forceinline__ void tmem_copy_scales_pair(unsigned addr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(addr), "l"(desc) : "memory");
+}
 // Arrive on the barrier at this address in both CTAs once the products are done.
 __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
   asm volatile(
@@ -102,24 +118,30 @@ __global__ void __launch_bounds__(256) permute_rows_kernel(const GemmParams p, _
   }
 }
 
-template <bool GATED, int SRC>
+template <bool FP8, bool GATED, int SRC>
 __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
     pair_kernel(const __grid_constant__ GemmParams p, const __grid_constant__ CUtensorMap tm_w,
-                const __grid_constant__ CUtensorMap tm_x) {
+                const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_ws,
+                const __grid_constant__ CUtensorMap tm_xs) {
+  static_assert(!FP8 || (!GATED && SRC == kDense), "MXFP8: plain dense products only");
   extern __shared__ unsigned char raw[];
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
   __shared__ unsigned tmem_slot;
   constexpr int kAcc = GATED ? 2 : 1;
+  constexpr int kElems = FP8 ? 128 : 64;             // K elements of a stage's 128-byte rows
+  constexpr int kScales = FP8 ? (1 + 2) * 512 : 0;   // a stage's scale tiles: 128 weight rows, 256 token rows
+  constexpr int kScaleCols = FP8 ? (1 + 2) * 4 : 0;  // and their columns of tensor memory
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(kFull, tid >> 5, 0);  // uniform
   const int rank = blockIdx.x & 1;
   const int x_bytes = p.bn / 2 * 128;  // bn is a multiple of 32: whole 8-row swizzle groups
   const unsigned smem0 = (smem_u32(raw) + 1023u) & ~1023u;
   const unsigned x0 = smem0 + p.stages * (kAcc * kATile);
+  const unsigned sf0 = x0 + p.stages * x_bytes;
   int* first = nullptr;
   int* off = nullptr;
   if constexpr (SRC != kDense) {
-    first = reinterpret_cast<int*>(raw + (x0 - smem_u32(raw)) + p.stages * x_bytes);
+    first = reinterpret_cast<int*>(raw + (sf0 - smem_u32(raw)));
     off = first + p.experts + 1;
   }
   if (tid == 0) {
@@ -170,17 +192,23 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
       const int half = round32(t.ntok) / 2;
       const int wrow = (SRC == kDense ? 0 : t.expert * (kAcc * p.n)) + t.m * kPairTileM + rank * kTileM;
       const int xrow = t.tok0 + rank * half;
-      const unsigned bytes = kAcc * kATile + (SRC == kDense ? x_bytes : half * 128);
+      const unsigned bytes = kAcc * kATile + (SRC == kDense ? x_bytes : half * 128) + kScales;
       for (int kb = 0; kb < p.kblocks; ++kb) {
         if (!(ok = __all_sync(kFull, wait_for_cluster(&empty[s], ph, p)))) break;
         if (elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * bytes + p.extra_tx);
           const unsigned bar = bar0 + s * 8, dst = smem0 + s * (kAcc * kATile), xdst = x0 + s * x_bytes;
-          tma_load_2d_pair(dst, &tm_w, kb * 64, wrow, bar);
-          if constexpr (GATED) tma_load_2d_pair(dst + kATile, &tm_w, kb * 64, wrow + p.n, bar);
-          if constexpr (SRC == kDense) tma_load_2d_pair(xdst, &tm_x, kb * 64, xrow, bar);
+          tma_load_2d_pair(dst, &tm_w, kb * kElems, wrow, bar);
+          if constexpr (GATED) tma_load_2d_pair(dst + kATile, &tm_w, kb * kElems, wrow + p.n, bar);
+          if constexpr (SRC == kDense) tma_load_2d_pair(xdst, &tm_x, kb * kElems, xrow, bar);
+          if constexpr (FP8) {  // scale tiles are 128 rows; of the token rows each CTA needs all
+            const unsigned sf = sf0 + s * kScales;
+            tma_load_2d_pair(sf, &tm_ws, 0, (t.m * 2 + rank) * p.kblocks + kb, bar);
+            for (int r = 0; r < 2; ++r)
+              tma_load_2d_pair(sf + 512 + r * 512, &tm_xs, 0, (t.tok0 / 128 + r) * p.kblocks + kb, bar);
+          }
           if constexpr (SRC == kGrouped)
-            for (int r = 0; r < half; r += 16) tma_load_2d_pair(xdst + r * 128, &tm_x, kb * 64, xrow + r, bar);
+            for (int r = 0; r < half; r += 16) tma_load_2d_pair(xdst + r * 128, &tm_x, kb * kElems, xrow + r, bar);
         }
         __syncwarp();
         if (++s == p.stages) {
@@ -211,11 +239,20 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
           tcgen05_fence_after();
           if (elect_one()) {
             const unsigned a = a_lo + s * (kAcc * kATile / 16), b = b_lo + s * (x_bytes / 16);
+            const unsigned sf = tmem + p.nbuf * acc_cols + s * kScaleCols;
+            if constexpr (FP8) {
+#pragma unroll
+              for (int q = 0; q < 3; ++q)
+                tmem_copy_scales_pair(sf + 4 * q, desc_scales(sf0 + s * kScales + 512 * q));
+            }
 #pragma unroll
             for (int k = 0; k < 4; ++k)
 #pragma unroll
               for (int q = 0; q < kAcc; ++q)
-                mma_bf16_pair(d + q * p.bn, a + q * (kATile / 16) + 2 * k, b + 2 * k, idesc, k > 0 || kb > 0);
+                if constexpr (FP8)
+                  mma_mxf8_pair(d, a + 2 * k, b + 2 * k, idesc | (k << 4) | (k << 29), sf, sf + 4, k > 0 || kb > 0);
+                else
+                  mma_bf16_pair(d + q * p.bn, a + q * (kATile / 16) + 2 * k, b + 2 * k, idesc, k > 0 || kb > 0);
             mma_commit_pair(&empty[s]);
             if (kb == p.kblocks - 1) mma_commit_pair(&acc_full[buf]);
           }

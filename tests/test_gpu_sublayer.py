@@ -72,6 +72,9 @@ def test_linear_bf16(R, K, N, act, bias, res, out):
     (128, 2048, 128, "none", False, True, torch.float32),
     (129, 160, 256, "swiglu", False, True, torch.float32),
     (300, 512, 700, "relu", True, False, torch.bfloat16),
+    (257, 160, 1000, "silu", True, True, torch.float32),
+    (700, 1056, 2100, "none", False, True, torch.bfloat16),
+    (3000, 128, 300, "gelu", True, False, torch.float32),
 ])
 def test_linear_mxfp8(R, K, N, act, bias, res, out):
     g = gen(R * 11 + K)
