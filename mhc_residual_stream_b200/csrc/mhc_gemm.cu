@@ -634,6 +634,8 @@ __global__ void __launch_bounds__(kGemmThreads, CTAS)
     if (clustered) pass_cluster_barriers(p.apart);
   } else if (warp == 1) {
     // ------------------------------------------------ products
+    // The bounded waits start with the operands' copies: the kernel before may take long.
+    if constexpr (SRC != kGather) griddep_wait();
     const unsigned a_lo = desc_lo(smem0), b_lo = desc_lo(x0), idesc = p.idesc;
     Segments it(sched);
     Segment g;
@@ -1057,6 +1059,8 @@ mhc_status mhc_linear(const void* x, const uint8_t* x_scale, int64_t x_stride, c
   const int64_t row_bytes = fp8 ? 1 : 2;
   if (x_stride < in_features || (x_stride * row_bytes) % 16 != 0 || out_stride < out_features ||
       (residual && residual_stride < out_features))
+    return MHC_ERR_INVALID_ARG;
+  if (static_cast<const void*>(residual) == out && (out_fp32 || residual_stride != out_stride))
     return MHC_ERR_INVALID_ARG;
   if (!workspace || !aligned(workspace, 256) || ws_bytes < mhc_linear_workspace_bytes(rows)) return MHC_ERR_WORKSPACE;
   GemmParams p{};

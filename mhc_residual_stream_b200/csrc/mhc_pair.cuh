@@ -223,6 +223,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------ products
+    griddep_wait();  // as in gemm_kernel, before the first bounded wait
     if (rank == 0) {
       const unsigned a_lo = desc_lo(smem0), b_lo = desc_lo(x0);
       int s = 0, buf = 0;

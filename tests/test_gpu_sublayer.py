@@ -48,6 +48,10 @@ LINEAR = [  # rows, K, N, activation, bias, residual, out
     (193, 72, 513, "swiglu", True, True, torch.bfloat16),
     (1000, 136, 300, "swiglu", False, False, torch.float32),
     (2500, 320, 777, "silu", True, False, torch.float32),
+    (600, 200, 4501, "swiglu", True, True, torch.bfloat16),
+    (200, 72, 9500, "none", True, True, torch.bfloat16),
+    (700, 136, 5001, "gelu", False, True, torch.bfloat16),
+    (65535, 16, 3, "none", True, False, torch.bfloat16),
 ]
 
 
@@ -201,6 +205,55 @@ def test_linear_wait_that_runs_out_is_reported():
     M.mhc_workspace_init(ws)
     assert torch.equal(run_linear(x, w, workspace=ws), want)
     assert M.mhc_get_device_status(ws) == M.OK
+
+
+def test_linear_behind_a_long_call():
+    # the bounded waits of a call that starts early do not run while the one before does
+    g = gen(15)
+    big_x, big_w = torch.zeros(16384, 8192, dtype=torch.bfloat16, device=DEV), torch.zeros(
+        16384, 8192, dtype=torch.bfloat16, device=DEV)
+    big_out = torch.empty(16384, 16384, dtype=torch.bfloat16, device=DEV)
+    x, w = bf((8, 512), g).to(DEV), bf((256, 512), g, 0.05).to(DEV)
+    want = run_linear(x, w)
+    wss = [M.new_linear_workspace(16384, DEV) for _ in range(3)]
+    out = [torch.empty_like(want) for _ in range(2)]
+    M.mhc_linear(big_x, big_w, big_out, workspace=wss[0])
+    torch.cuda.synchronize()
+    old = M.mhc_debug_set_wait(1_500_000, 0)  # 1.5 ms; the long call takes about 3
+    try:
+        M.mhc_linear(big_x, big_w, big_out, workspace=wss[0])
+        M.mhc_linear(x, w, out[0], workspace=wss[1])
+        M.mhc_linear(x, w, out[1], workspace=wss[2])
+        assert [M.mhc_get_device_status(ws) for ws in wss] == [M.OK] * 3
+    finally:
+        M.mhc_debug_set_wait(old, 0)
+    assert torch.equal(out[0], want) and torch.equal(out[1], want)
+
+
+def test_first_calls_may_be_captured():
+    import subprocess
+    import sys
+    code = """
+import torch
+from mhc_residual_stream_b200 import mhc as M
+from mhc_residual_stream_b200.moe import MoeConfig, MoeSublayer, MoeWeights
+cfg = MoeConfig(experts=8, intermediate=64, top_k=2)
+m, w = MoeSublayer(cfg, 40, 128), MoeWeights.draw(cfg, 128, 1, "cuda")
+x = torch.randn(40, 128, device="cuda").bfloat16()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    m.run(x, w)
+g.replay()
+torch.cuda.synchronize()
+a = [t.clone() for t in (m.logits, m.e2p, m.gemm2_permuted, m.shared_output)]
+m.run(x, w)
+torch.cuda.synchronize()
+assert m.device_status() == M.OK
+assert all(torch.equal(p, q) for p, q in zip(a, (m.logits, m.e2p, m.gemm2_permuted, m.shared_output)))
+print("captured first")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
 
 
 # ---------------------------------------------------------------- routing

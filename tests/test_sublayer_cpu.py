@@ -40,7 +40,8 @@ def test_linear_refusals(L):
     for kw in (dict(x=None), dict(w=None), dict(out=None), dict(xs=a), dict(wsc=a), dict(act=5), dict(act=-1),
                dict(x=_a(0x10008)), dict(w=_a(0x10008)), dict(xs=_a(0x10008), wsc=a), dict(bias=_a(0x10002)),
                dict(res=_a(0x10001), rst=100), dict(out=_a(0x10002), fp32=1), dict(xst=56), dict(xst=68),
-               dict(xs=a, wsc=a, xst=72), dict(ost=99), dict(res=a, rst=99)):
+               dict(xs=a, wsc=a, xst=72), dict(ost=99), dict(res=a, rst=99),
+               dict(res=a, rst=104), dict(res=a, rst=100, fp32=1)):  # the residual is out: same stride, bf16
         assert call(**kw) == M.INVALID_ARG, kw
     for kw in (dict(ws=None), dict(ws=_a(0x10010)), dict(wsb=M.mhc_linear_workspace_bytes(4) - 1)):
         assert call(**kw) == M.WORKSPACE, kw
