@@ -15,10 +15,10 @@
 //   warps 2-9   each CTA: epilogue of its 128 weight rows, two warps to a quarter of them
 //               (a gated tile of 256 columns fills tensor memory, so nothing hides it)
 // The experts' first product reads its token rows from a copy in permuted order
-// (permute_rows_kernel): the tensor-map gather moves four rows per 65 cycles, an
-// eighth of what a tile of 128 columns needs (2.16 ms against 0.75 for the product
-// of 16384 rows by 32 experts' 4096 x 7168), and 16-byte asynchronous copies by
-// four more warps kept too few bytes in flight (1.67 ms). The copy takes 0.05 ms.
+// (permute_rows_kernel): the tensor-map gather moves four rows per 65 cycles, a quarter
+// of what a tile of 128 columns needs (2.16 ms against 0.82 for the product of 16384
+// rows by 32 experts' 4096 x 7168), and 16-byte asynchronous copies by four more warps
+// kept too few bytes in flight (1.67 ms). The copy takes 0.05 ms.
 #pragma once
 
 namespace mhc {
