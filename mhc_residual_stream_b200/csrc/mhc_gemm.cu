@@ -847,6 +847,10 @@ mhc_status launch_gemm(GemmParams& p, const CUtensorMap& w, const CUtensorMap& x
   constexpr int acc = GATED ? 2 : 1;
   const int fixed = 1024 + (SRC == kDense ? 0 : 8 * (p.experts + 1));
   const int stage = acc * kATile + p.bn * 128 + (FP8 ? (acc + 1) * 512 : 0);
+  // Tensor memory: an allocation never waits for a CTA of another launch. A kernel of one
+  // CTA an SM takes more than half of the shared memory (12 stages or what fits), so it
+  // shares no SM; of the others at most two fit, with half of the columns each. (Two
+  // clusters that waited for each other's columns would wait for good.)
   const int limit = CTAS == 2 ? kHalfSmem : kGemmSmem - kStaticSmem;
   // A cluster's sums: apart from the ring where one CTA has the SM's memory (0.25 us
   // less than in the drained ring, which takes a barrier more on the way), in the ring

@@ -190,20 +190,23 @@ def test_linear_on_a_side_stream_and_in_a_graph():
             assert torch.equal(out, want)
 
 
-def test_linear_wait_that_runs_out_is_reported():
+@pytest.mark.parametrize("R,K,N,act", [(8, 512, 256, "none"), (8, 4096, 512, "swiglu"), (600, 200, 4500, "swiglu"),
+                                       (4099, 64, 64, "none")])
+def test_linear_wait_that_runs_out_is_reported(R, K, N, act):
+    # a cluster, a pair and whole tiles: the copies are expected to bring more than they do
     g = gen(12)
-    x, w = bf((8, 512), g).to(DEV), bf((256, 512), g, 0.05).to(DEV)
-    want = run_linear(x, w)
-    ws = M.new_linear_workspace(8, DEV)
+    x, w = bf((R, K), g).to(DEV), bf((2 * N if act == "swiglu" else N, K), g, 0.05).to(DEV)
+    want = run_linear(x, w, act=act)
+    ws = M.new_linear_workspace(R, DEV)
     torch.cuda.synchronize()
     old = M.mhc_debug_set_wait(2_000_000, 4)
     try:
-        run_linear(x, w, workspace=ws)
+        run_linear(x, w, act=act, workspace=ws)
         assert M.mhc_get_device_status(ws) == M.DEVICE_TIMEOUT
     finally:
         M.mhc_debug_set_wait(old, 0)
     M.mhc_workspace_init(ws)
-    assert torch.equal(run_linear(x, w, workspace=ws), want)
+    assert torch.equal(run_linear(x, w, act=act, workspace=ws), want)
     assert M.mhc_get_device_status(ws) == M.OK
 
 
@@ -444,6 +447,22 @@ def test_experts_report_bad_indices(R):
         out, ws = run_experts(x, w13, w2, prow, np.array(o))  # nothing is computed
         assert M.mhc_get_device_status(ws) == M.DEVICE_INDEX
         assert bool((out == 5.0).all())
+
+
+@pytest.mark.parametrize("R,k,E,H,I", [(3, 2, 8, 2048, 256), (300, 2, 4, 128, 264)])
+def test_experts_wait_that_runs_out_is_reported(R, k, E, H, I):
+    x, w13, w2, e2p, prow, off = draw_experts(R, k, E, H, I, seed=9)
+    want, ws = run_experts(x, w13, w2, prow, off)
+    torch.cuda.synchronize()
+    old = M.mhc_debug_set_wait(2_000_000, 4)
+    try:
+        run_experts(x, w13, w2, prow, off, workspace=ws)
+        assert M.mhc_get_device_status(ws) == M.DEVICE_TIMEOUT
+    finally:
+        M.mhc_debug_set_wait(old, 0)
+    M.mhc_workspace_init(ws)
+    assert torch.equal(run_experts(x, w13, w2, prow, off, workspace=ws)[0], want)
+    assert M.mhc_get_device_status(ws) == M.OK
 
 
 # ---------------------------------------------------------------- a run of them together
