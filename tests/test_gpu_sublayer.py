@@ -94,6 +94,36 @@ def test_linear_mxfp8(R, K, N, act, bias, res, out):
     assert_within(got, exact, bound, f"mxfp8 linear {R}x{K}x{N} {act}")
 
 
+# One product for every form the library chooses between: whole tiles, pairs, and
+# clusters of 2-8 CTAs at one and two CTAs an SM.
+FORMS = {
+    (False, False): [(77, 64, 1), (130, 1024, 1000), (100, 768, 1500), (1, 768, 1), (17, 768, 4000), (17, 1024, 2500),
+                     (1, 1536, 1), (130, 1536, 300), (1, 1536, 4000), (1, 2048, 1), (256, 2048, 1), (31, 520, 100)],
+    (False, True): [(77, 64, 1), (130, 1024, 1000), (40, 1536, 4000), (17, 768, 4000), (1, 768, 1), (17, 768, 2500),
+                    (17, 2048, 2500), (1, 1024, 1), (1, 1536, 4000), (1, 1536, 1), (256, 1536, 1)],
+    (True, False): [(130, 64, 1), (1, 1536, 1), (1, 2048, 1), (100, 4096, 2000), (1, 4096, 1), (1, 4096, 2000),
+                    (300, 4096, 2000)],
+    (True, True): [(1, 1536, 128), (1, 2048, 128), (1, 4096, 128), (1, 2048, 4096), (40, 544, 256), (400, 64, 128)],
+}
+
+
+@pytest.mark.parametrize("fp8,gated,R,K,N", [(*k, *s) for k, v in FORMS.items() for s in v])
+def test_linear_every_form(fp8, gated, R, K, N):
+    g = gen(R + 3 * K + 7 * N)
+    act, W = ("swiglu", 2 * N) if gated else ("silu", N)
+    b, r = torch.randn(W, generator=g) * 0.3, bf((R, N), g)
+    if fp8:
+        xd, xs, x = mxfp8(torch.randn(R, K, generator=g) * torch.exp2(torch.randint(-4, 5, (R, 1), generator=g).float()))
+        wd, wsc, w = mxfp8(torch.randn(W, K, generator=g) * (1.5 / K ** 0.5))
+        ops = [(d.to(DEV), sc.to(DEV), True) for d, sc in ((xd, xs), (wd, wsc))]
+    else:
+        x, w = bf((R, K), g), bf((W, K), g, 1.5 / K ** 0.5)
+        ops, x, w = [x.to(DEV), w.to(DEV)], f64(x), f64(w)
+    got = run_linear(*ops, b.to(DEV), act, r.to(DEV), torch.float32)
+    exact, bound = linear_bound(x, w, f64(b), act, f64(r), torch.float32)
+    assert_within(got, exact, bound, f"{R}x{K}x{N}")
+
+
 def test_linear_takes_what_the_quantizer_writes():
     g = gen(3)
     x, w = bf((70, 384), g), bf((256, 384), g, 0.1)
