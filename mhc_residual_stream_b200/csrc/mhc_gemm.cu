@@ -97,30 +97,28 @@ struct Schedule {
   int kb, grid, cta, waves, base, parts, total, a, b;
 
   // One tile per cluster of `split` CTAs, its K divided evenly.
-  __device__ Schedule(int kblocks, int split) {
-    kb = kblocks;
-    grid = gridDim.x;
-    cta = blockIdx.x;
-    waves = base = total = 0;
-    parts = split;
-    const int r = cta % split, t0 = cta / split * kb;
-    a = t0 + static_cast<int>(static_cast<int64_t>(r) * kb / split);
-    b = t0 + static_cast<int>(static_cast<int64_t>(r + 1) * kb / split);
+  __device__ static Schedule by_cluster(int kblocks, int split) {
+    Schedule s{kblocks, static_cast<int>(gridDim.x), static_cast<int>(blockIdx.x), 0, 0, split, 0, 0, 0};
+    const int r = s.cta % split, t0 = s.cta / split * s.kb;
+    s.a = t0 + static_cast<int>(static_cast<int64_t>(r) * s.kb / split);
+    s.b = t0 + static_cast<int>(static_cast<int64_t>(r + 1) * s.kb / split);
+    return s;
   }
-  __device__ Schedule(int tiles, int kblocks, int max_split, int) {
-    kb = kblocks;
-    grid = gridDim.x;
-    cta = blockIdx.x;
-    waves = tiles / grid;
-    base = waves * grid;
-    const int rest = tiles - base;
-    total = rest * kb;
+  __device__ static Schedule by_tile(int tiles, int kblocks, int max_split) {
+    Schedule s{kblocks, static_cast<int>(gridDim.x), static_cast<int>(blockIdx.x), 0, 0, 0, 0, 0, 0};
+    s.waves = tiles / s.grid;
+    s.base = s.waves * s.grid;
+    const int rest = tiles - s.base;
+    s.total = rest * s.kb;
     // A share of less than kMinShare K blocks is not worth the join (both products of 37
     // rows by 24 experts' 328 x 712: 30 us with shares of 2 and more, 20 without); none
     // is empty.
-    parts = min(min(grid, rest * max_split), max(rest, total / kMinShare));
-    a = cta < parts ? static_cast<int>(static_cast<int64_t>(cta) * total / parts) : 0;
-    b = cta < parts ? static_cast<int>(static_cast<int64_t>(cta + 1) * total / parts) : 0;
+    s.parts = min(min(s.grid, rest * max_split), max(rest, s.total / kMinShare));
+    if (s.cta < s.parts) {
+      s.a = s.start_of(s.cta);
+      s.b = s.start_of(s.cta + 1);
+    }
+    return s;
   }
   __device__ int start_of(int c) const { return static_cast<int>(static_cast<int64_t>(c) * total / parts); }
   // the CTA whose share holds flattened block w
@@ -540,7 +538,8 @@ __global__ void __launch_bounds__(kGemmThreads, CTAS)
   if constexpr (SRC == kGather) griddep_launch_dependents();
   if constexpr (SRC != kDense) tiles = first[p.experts];
   const unsigned tmem = tmem_slot;
-  const Schedule sched = clustered ? Schedule(p.kblocks, p.max_split) : Schedule(tiles, p.kblocks, p.max_split, 0);
+  const Schedule sched =
+      clustered ? Schedule::by_cluster(p.kblocks, p.max_split) : Schedule::by_tile(tiles, p.kblocks, p.max_split);
   const int acc_cols = kAcc * p.bn;  // of one tile
 
   if (warp == 0) {

@@ -507,19 +507,35 @@ def mxfp8_quantize_rows(x, data, scale, swizzled_128x4: bool = True, stream=None
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
-def _arg(t, dtype, dims, name, dev, contiguous=True):
-    """The address of an argument (None for None) after its checks: a CUDA tensor on
-    device `dev` (the current one, whose stream the call runs on) of the given type
-    and dims. One pass, for calls of a few microseconds."""
+def _arg(t, dtype, name, dev):
+    """The address of a contiguous CUDA tensor of the given type on device `dev` (the
+    current one, whose stream the call runs on). The checks of a call of a few
+    microseconds: four attribute reads; the callers compare shapes."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _refuse(t, dtype, name, dev, True)
+
+
+def _arg_rows(t, dtype, name, dev):
+    """_arg of a matrix whose rows may be strided (_row_stride checks them)."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.dim() == 2:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _refuse(t, dtype, name, dev, False)
+
+
+def _refuse(t, dtype, name, dev, contiguous):
+    _need(t, dtype, name, None if contiguous else 2)
     if t is None:
-        return None
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.dim() != dims or t.get_device() != dev \
-            or (contiguous and not t.is_contiguous()):
-        _need(t, dtype, name, dims)
-        if contiguous:
-            _contig(t, name)
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
-    return t.data_ptr()
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if contiguous:
+        _contig(t, name)
+    raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
 
 
 def _device() -> int:
@@ -535,7 +551,7 @@ def _raw_stream(stream, dev: int) -> int:
 def _ws(t, dev):
     if t is None:
         return None, 0
-    return _arg(t, _U8, 1, "workspace", dev), t.shape[0]
+    return _arg(t, _U8, "workspace", dev), t.numel()
 
 
 def _workspace(n: int, where: str, device):
@@ -562,15 +578,14 @@ def new_linear_workspace(rows: int, device=None) -> torch.Tensor:
     return _workspace(mhc_linear_workspace_bytes(rows), "mhc_linear_workspace_bytes", device)
 
 
-def _operand(v, name, dev, contiguous):
+def _operand(v, name, dev, arg):
     """(data, address, scale address) of a bf16 matrix, or of an MXFP8 one given as
-    (data, scale, swizzled)."""
+    (data, scale, swizzled); arg: _arg or _arg_rows."""
     if isinstance(v, torch.Tensor):
-        return v, _arg(v, _BF16, 2, name, dev, contiguous), None
+        return v, arg(v, _BF16, name, dev), None
     data, scale, swizzled = v
-    pd = _arg(data, _U8, 2, name + " data", dev, contiguous)
-    _need(scale, _U8, name + " scale")
-    ps = _arg(scale, _U8, scale.dim(), name + " scale", dev)
+    pd = arg(data, _U8, name + " data", dev)
+    ps = _arg(scale, _U8, name + " scale", dev)
     if not swizzled:
         raise ValueError(f"{name} scales must be in the swizzled 128x4 layout")
     R, K = data.shape
@@ -589,19 +604,19 @@ def mhc_linear(x, weight, out, bias=None, activation: str = "none", residual=Non
     if act is None:
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
     dev = _device()
-    xd, px, pxs = _operand(x, "x", dev, False)
-    wd, pw, pws = _operand(weight, "weight", dev, True)
+    xd, px, pxs = _operand(x, "x", dev, _arg_rows)
+    wd, pw, pws = _operand(weight, "weight", dev, _arg)
     if (pxs is None) != (pws is None):
         raise TypeError("x and weight must both be bf16 or both MXFP8")
     fp32 = isinstance(out, torch.Tensor) and out.dtype is _F32
-    po = _arg(out, _F32 if fp32 else _BF16, 2, "out", dev, False)
-    pb = _arg(bias, _F32, 1, "bias", dev)
-    pr = _arg(residual, _BF16, 2, "residual", dev, False)
+    po = _arg_rows(out, _F32 if fp32 else _BF16, "out", dev)
+    pb = None if bias is None else _arg(bias, _F32, "bias", dev)
+    pr = None if residual is None else _arg_rows(residual, _BF16, "residual", dev)
     pws_, wsb = _ws(workspace, dev)
     R, K = xd.shape
     ro, N = out.shape
     W = 2 * N if act == 4 else N
-    if wd.shape != (W, K) or ro != R or (pb is not None and bias.shape[0] != W) \
+    if wd.shape != (W, K) or ro != R or (pb is not None and bias.shape != (W,)) \
             or (pr is not None and residual.shape != (R, N)):
         raise ValueError("x/weight/bias/residual/out shapes disagree")
     st = (_lib or lib()).mhc_linear(px, pxs, _row_stride(xd, "x"), pw, pws, pb, act, pr,
@@ -631,19 +646,20 @@ def mhc_moe_route(logits, expert_weights, expert_ids, expanded_idx_to_permuted_i
         raise ValueError(f"scoring must be one of {sorted(SCORES)}")
     dev = _device()
     bf16 = isinstance(logits, torch.Tensor) and logits.dtype is _BF16
-    pl = _arg(logits, _BF16 if bf16 else _F32, 2, "logits", dev)
-    pb = _arg(bias, _F32, 1, "bias", dev)
-    pw = _arg(expert_weights, _F32, 2, "expert_weights", dev)
-    pi = _arg(expert_ids, _I32, 2, "expert_ids", dev)
-    pe = _arg(expanded_idx_to_permuted_idx, _I32, 1, "expanded_idx_to_permuted_idx", dev)
-    pp = _arg(permuted_rows, _I32, 1, "permuted_rows", dev)
-    po = _arg(expert_offsets, _I32, 1, "expert_offsets", dev)
+    pl = _arg(logits, _BF16 if bf16 else _F32, "logits", dev)
+    pb = None if bias is None else _arg(bias, _F32, "bias", dev)
+    pw = _arg(expert_weights, _F32, "expert_weights", dev)
+    pi = _arg(expert_ids, _I32, "expert_ids", dev)
+    pe = _arg(expanded_idx_to_permuted_idx, _I32, "expanded_idx_to_permuted_idx", dev)
+    pp = _arg(permuted_rows, _I32, "permuted_rows", dev)
+    po = _arg(expert_offsets, _I32, "expert_offsets", dev)
     pws, wsb = _ws(workspace, dev)
     R, E = logits.shape
     rw, k = expert_weights.shape
-    if rw != R or expert_ids.shape != (R, k) or expanded_idx_to_permuted_idx.shape[0] != R * k \
-            or permuted_rows.shape[0] != R * k or expert_offsets.shape[0] != E + 1 \
-            or (pb is not None and bias.shape[0] != E):
+    pairs = (R * k,)
+    if rw != R or expert_ids.shape != (R, k) or expanded_idx_to_permuted_idx.shape != pairs \
+            or permuted_rows.shape != pairs or expert_offsets.shape != (E + 1,) \
+            or (pb is not None and bias.shape != (E,)):
         raise ValueError("MoE route shapes disagree")
     a = RouteArgs(score, num_groups, top_groups, group_top, k, renormalize, weight_scale)
     st = (_lib or lib()).mhc_moe_route(pl, bf16, pb, ctypes.byref(a), pw, pi, pe, pp, po, R, E, pws, wsb,
@@ -666,17 +682,17 @@ def mhc_moe_experts(x, w13, w2, permuted_rows, expert_offsets, gemm2_permuted, w
     """gemm2_permuted [P, H] of the permuted rows: w2[e] (silu(gate) * up) with gate and up
     from w13[e] [2I, H] and the rows x[permuted_rows], expert by expert (expert_offsets)."""
     dev = _device()
-    px = _arg(x, _BF16, 2, "x", dev, False)
-    p13 = _arg(w13, _BF16, 3, "w13", dev)
-    p2 = _arg(w2, _BF16, 3, "w2", dev)
-    pp = _arg(permuted_rows, _I32, 1, "permuted_rows", dev)
-    po = _arg(expert_offsets, _I32, 1, "expert_offsets", dev)
-    pg = _arg(gemm2_permuted, _BF16, 2, "gemm2_permuted", dev)
+    px = _arg_rows(x, _BF16, "x", dev)
+    p13 = _arg(w13, _BF16, "w13", dev)
+    p2 = _arg(w2, _BF16, "w2", dev)
+    pp = _arg(permuted_rows, _I32, "permuted_rows", dev)
+    po = _arg(expert_offsets, _I32, "expert_offsets", dev)
+    pg = _arg(gemm2_permuted, _BF16, "gemm2_permuted", dev)
     pws, wsb = _ws(workspace, dev)
     R, H = x.shape
     E, h2, I = w2.shape
-    P = permuted_rows.shape[0]
-    if w13.shape != (E, 2 * I, H) or h2 != H or expert_offsets.shape[0] != E + 1 or gemm2_permuted.shape != (P, H):
+    P, = permuted_rows.shape
+    if w13.shape != (E, 2 * I, H) or h2 != H or expert_offsets.shape != (E + 1,) or gemm2_permuted.shape != (P, H):
         raise ValueError("MoE experts shapes disagree")
     st = (_lib or lib()).mhc_moe_experts(px, _row_stride(x, "x"), p13, p2, pp, po, pg, R, P, E, H, I, pws, wsb,
                                _raw_stream(stream, dev))

@@ -289,6 +289,30 @@ print("captured first")
     assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
 
 
+def test_linear_binding_refusals():
+    x, w = torch.zeros(4, 64, dtype=torch.bfloat16, device=DEV), torch.zeros(32, 64, dtype=torch.bfloat16, device=DEV)
+    out, ws = torch.zeros(4, 32, dtype=torch.bfloat16, device=DEV), M.new_linear_workspace(4, DEV)
+    d, s = torch.zeros(4, 64, dtype=torch.uint8, device=DEV), torch.zeros(512, dtype=torch.uint8, device=DEV)
+    for a, kw in (((x.float(), w, out), {}), ((x, w.float(), out), {}), ((x, w, out.half()), {}), ((x.cpu(), w, out), {}),
+                  (((d, s, True), w, out), {}), ((x, w, out), dict(bias=out)), ((x, w, out), dict(residual=x.float())),
+                  ((x, w, out), dict(workspace=ws.float()))):
+        with pytest.raises(TypeError):
+            M.mhc_linear(*a, **{"workspace": ws, **kw})
+    for a, kw in (((x, w[:, ::2], out), {}), ((x[:, ::2], w, out), {}), ((x, w, out[:3]), {}), ((x, w, out[:, :31]), {}),
+                  ((x, w, out), dict(bias=torch.zeros(31, device=DEV))), ((x, w, out), dict(residual=out[:2])),
+                  ((x, w, out), dict(activation="swiglu")), ((x[0], w, out), {}),
+                  (((d, s, False), (d, s, False), out), {}), (((d, s[:511], True), (d, s, True), out), {})):
+        with pytest.raises(ValueError):
+            M.mhc_linear(*a, **{"workspace": ws, **kw})
+    for a, kw, st in (((x, w, out), dict(workspace=None), M.WORKSPACE), ((x, w, out), dict(workspace=ws[:256]), M.WORKSPACE),
+                      ((x[:, 1:57], w[:, :56].contiguous(), out), {}, M.INVALID_ARG),
+                      ((x[:0], w, out[:0]), {}, M.UNSUPPORTED_SHAPE),
+                      ((x, w, torch.zeros(32, dtype=torch.bfloat16, device=DEV).expand(4, 32)), {}, M.INVALID_ARG)):
+        with pytest.raises(M.MhcError) as e:
+            M.mhc_linear(*a, **{"workspace": ws, **kw})
+        assert e.value.status == st
+
+
 # ---------------------------------------------------------------- routing
 
 def check_route(logits, k, bias=None, **kw):

@@ -111,6 +111,10 @@ def test_binding_refuses_cpu_tensors_and_unknown_names(L):
         M.mhc_moe_route(x, x, x, x, x, x, scoring="linear")
     with pytest.raises(TypeError):
         M.mhc_moe_experts(x, x, x, x, x, x)
+    with pytest.raises(TypeError):
+        M.mhc_linear(None, x, x)
+    with pytest.raises(TypeError):
+        M.mhc_linear((x, x, True), x, x)  # MXFP8 data are bytes
 
 
 # ---------------------------------------------------------------- the oracle
