@@ -77,9 +77,9 @@ __device__ __forceinline__ float key_value(unsigned k) {
 // within 2 + 1.17 |l| steps of the exponential, which moves the sigmoid by at most a
 // quarter of the first and 0.23 of the second; an addition and __fdividef's 2 steps
 // follow), an exponential over a sum of up to 1024 by 50 times the largest of the row;
-// a bias adds one rounding. A group's value is the sum of two choices: twice that.
-__device__ __forceinline__ bool too_near(float a, float b, float unit) {
-  return !(fabsf(a - b) > 0x1p-22f * (unit + fabsf(a) + fabsf(b)));
+// a bias adds one rounding. mag: the magnitudes that were rounded on both sides.
+__device__ __forceinline__ bool too_near(float a, float b, float units, float mag) {
+  return !(fabsf(a - b) > 0x1p-24f * (units + mag));
 }
 
 __device__ __forceinline__ float load_logit(const float* p) { return *p; }
@@ -166,14 +166,17 @@ __device__ __forceinline__ unsigned keep_groups(const RouteParams& p, const floa
     v2 = fmaxf(fmaxf(v2, w2), fminf(v1, w1));
     v1 = fmaxf(v1, w1);
   }
-  const float value = p.group_top == 2 && v2 > -INFINITY ? v1 + v2 : v1;
+  const bool two = p.group_top == 2 && v2 > -INFINITY;
+  const float value = two ? v1 + v2 : v1;
+  const float mag = two ? fabsf(v1) + fabsf(v2) + fabsf(value) : fabsf(v1);  // two choices of opposite sign may cancel
   int rank;
   const unsigned mask = best_groups(p, order_key(value), lane, &rank);
   if (p.top_groups < G) {
     const unsigned in = __ballot_sync(kFull, g < G && sub == 0 && rank == p.top_groups - 1);
     const unsigned out = __ballot_sync(kFull, g < G && sub == 0 && rank == p.top_groups);
     const float a = __shfl_sync(kFull, value, __ffs(in) - 1), b = __shfl_sync(kFull, value, __ffs(out) - 1);
-    *near = b > -INFINITY && too_near(a, b, unit);
+    const float ma = __shfl_sync(kFull, mag, __ffs(in) - 1), mb = __shfl_sync(kFull, mag, __ffs(out) - 1);
+    *near = b > -INFINITY && too_near(a, b, 4.f * unit, ma + mb);
   }
   return mask;
 }
@@ -263,6 +266,28 @@ __device__ __noinline__ int choose_exact(const RouteParams& p, const T* src, int
   return id;
 }
 
+// The first n winners of a row (lane t: the t-th), ordered by their choices in 64 bits:
+// sigmoid scores need the winners' own logits only. (8191 rows x 200 experts have some
+// 16 rows with two winners too near; choosing those again in full took 12 us of 32.)
+template <typename T>
+__device__ __noinline__ int order_exact(const RouteParams& p, const T* src, int lane, int n, int id) {
+  double d = 0.0;
+  if (lane < n) d = 1.0 / (1.0 + exp(-static_cast<double>(load_logit(src + id)))) + static_cast<double>(p.bias[id]);
+  int rank = 0;
+  for (int o = 0; o < n; ++o) {
+    const double w = __shfl_sync(kFull, d, o);
+    const int e = __shfl_sync(kFull, id, o);
+    rank += w > d || (w == d && e < id) ? 1 : 0;
+  }
+  if (lane >= n) rank = 32;
+  int sorted = -1;
+  for (int o = 0; o < n; ++o) {
+    const int r = __shfl_sync(kFull, rank, o), e = __shfl_sync(kFull, id, o);
+    if (r == lane) sorted = e;
+  }
+  return sorted;
+}
+
 // One row: ids and weights; the row's pairs are counted in `count` (shared memory).
 template <typename T, int V>
 __device__ __forceinline__ void choose_row(const RouteParams& p, int row, int lane, double* choice, int* count) {
@@ -325,8 +350,8 @@ __device__ __forceinline__ void choose_row(const RouteParams& p, int row, int la
 #pragma unroll
     for (int j = 0; j < V; ++j) key[j] = order_key(l[j]);
   }
-  // top-k: lane t keeps the t-th winner; with a bias one round more, to see how near
-  // the first that is not chosen comes. Up to 8 experts a lane are sorted first, so
+  // top-k: lane t keeps the t-th winner; with a bias further ones, as far as they are too
+  // near to the k-th to say which comes first. Up to 8 experts a lane are sorted first, so
   // that a round takes the head of the winning lane's list (39 instructions less).
   constexpr bool kSorted = V <= 8;
   int slot[V];
@@ -334,9 +359,10 @@ __device__ __forceinline__ void choose_row(const RouteParams& p, int row, int la
   for (int j = 0; j < V; ++j) slot[j] = j;
   if constexpr (kSorted) sort_keys<V>(key, slot);
   int id = -1;
-  float before = 0.f;
-  const int rounds = p.bias != nullptr ? p.k + 1 : p.k;
-  for (int t = 0; t < rounds; ++t) {
+  float before = 0.f, last = 0.f;  // the previous winner's choice, and the k-th's
+  int n = 0;                       // winners kept: k, and those after it that are too near to it
+  bool close = false;              // two neighbours are
+  for (; n < 32; ++n) {
     unsigned best = key[0];
     int at = slot[0];
     if constexpr (!kSorted) {
@@ -349,12 +375,16 @@ __device__ __forceinline__ void choose_row(const RouteParams& p, int row, int la
     }
     const unsigned winner = __reduce_max_sync(kFull, best);
     if (winner == 0) break;  // nothing is left
-    const unsigned e = __reduce_min_sync(kFull, best == winner ? static_cast<unsigned>(lane + 32 * at) : 0xffffffffu);
     if (p.bias != nullptr) {
       const float v = key_value(winner);
-      near |= t > 0 && too_near(before, v, unit);
+      if (n >= p.k && !too_near(last, v, 2.f * unit, fabsf(last) + fabsf(v))) break;
+      close |= n > 0 && too_near(before, v, 2.f * unit, fabsf(before) + fabsf(v));
       before = v;
+      if (n == p.k - 1) last = v;
+    } else if (n == p.k) {
+      break;
     }
+    const unsigned e = __reduce_min_sync(kFull, best == winner ? static_cast<unsigned>(lane + 32 * at) : 0xffffffffu);
     const bool mine = static_cast<unsigned>(lane + 32 * at) == e && best == winner;
     if constexpr (kSorted) {
 #pragma unroll
@@ -367,9 +397,10 @@ __device__ __forceinline__ void choose_row(const RouteParams& p, int row, int la
       for (int j = 0; j < V; ++j)
         if (mine && j == at) key[j] = 0;
     }
-    if (lane == t) id = static_cast<int>(e);
+    if (lane == n) id = static_cast<int>(e);
   }
-  if (near) id = choose_exact<T, V>(p, src, lane, choice, top);
+  if (near || (close && (p.softmax || n == 32))) id = choose_exact<T, V>(p, src, lane, choice, top);
+  else if (close) id = order_exact<T>(p, src, lane, n, id);
   if (lane >= p.k) id = -1;
   float chosen = id >= 0 ? load_logit(src + id) : -INFINITY;
   float w = 0.f;

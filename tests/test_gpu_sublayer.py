@@ -407,6 +407,28 @@ def test_route_near_equal_choices_do_not_depend_on_fp32_rounding():
     check_route(base + step, 8, torch.ones(E), scoring="softmax")
 
 
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_route_groups_whose_choices_cancel(scoring):
+    # a group's value is the sum of two choices a thousand away from zero on either side:
+    # fp32 sums would be off by more than the groups differ
+    R, G, S = 200, 8, 4
+    logits = torch.randn(R, G * S, generator=gen(21))
+    bias = torch.tensor([1000.0, -1000.0, -5000.0, -6000.0]).repeat(G)
+    check_route(logits, 4, bias, scoring=scoring, num_groups=G, top_groups=3, group_top=2)
+    bias = bias + torch.randn(G * S, generator=gen(22)) * 1e-4
+    check_route(logits, 6, bias, scoring=scoring, num_groups=G, top_groups=4, group_top=2)
+
+
+def test_route_many_near_winners():
+    # up to all experts within fp32's reach of each other: more than a warp's lanes can hold
+    g = gen(23)
+    for E, k in ((64, 8), (20, 4), (40, 16), (200, 3)):
+        base = torch.rand(30, 1, generator=g) * 2
+        step = 2.0 ** -22 * torch.stack([torch.randperm(E, generator=g) for _ in range(30)]).float()
+        check_route(base + step, k, torch.full((E,), 0.25), scoring="sigmoid")
+        check_route(base + step, k, torch.full((E,), -0.25), scoring="softmax")
+
+
 def test_route_bf16_logits():
     g = gen(13)
     logits = bf((130, 256), g, 2.0)
