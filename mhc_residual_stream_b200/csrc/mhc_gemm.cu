@@ -162,7 +162,8 @@ struct TileAt {
 // Tile index -> weight rows and tokens. Token tiles are innermost, so that the
 // tiles that read the same weights are neighbours in time.
 template <int SRC>
-__device__ __forceinline__ TileAt tile_at(const GemmParams& p, const int* first, const int* off, int tile) {
+__device__ __forceinline__ TileAt tile_at(const GemmParams& p, const int* first, const int* off, int tile,
+                                          const int* order = nullptr) {
   TileAt t;
   if constexpr (SRC == kDense) {
     const int tt = (p.rows + p.bn - 1) / p.bn;
@@ -179,60 +180,76 @@ __device__ __forceinline__ TileAt tile_at(const GemmParams& p, const int* first,
     }
     const int tt = (first[lo + 1] - first[lo]) / p.m_tiles;
     const int r = tile - first[lo];
-    t.expert = lo;
+    t.expert = order != nullptr ? order[lo] : lo;
     t.m = r / tt;
-    const int begin = off[lo], end = off[lo + 1];
+    const int begin = off[t.expert], end = off[t.expert + 1];
     t.tok0 = begin + (r - t.m * tt) * p.bn;
     t.ntok = min(p.bn, end - t.tok0);
   }
   return t;
 }
 
-// Grouped: the first tile and first permuted row of each expert, by one warp.
-__device__ __forceinline__ void expert_tiles(const GemmParams& p, int* first, int* off, int lane) {
-  int run = 0;
+__host__ __device__ constexpr int round32(int v) { return (v + 31) / 32 * 32; }
+
+// Rows of an expert's tiles in the pair kernel: nearly equal, multiples of 32 but the last.
+__device__ __forceinline__ int even_rows(int n, int bn) {
+  const int tt = (n + bn - 1) / bn;
+  return n > 0 ? round32((n + tt - 1) / tt) : 0;
+}
+
+// Grouped, by one warp: the first permuted row of each expert (off), the experts in the
+// order their tiles are taken in (`order`, or as they lie where it is null) and the first
+// tile of each place of that order.
+__device__ __forceinline__ void expert_tiles(const GemmParams& p, int* first, int* off, int* order, int lane) {
+  const int E = p.experts;
   bool bad = false;
-  for (int e0 = 0; e0 < p.experts; e0 += 32) {
-    const int e = e0 + lane;
-    int lo = 0, hi = 0;
-    if (e < p.experts) {
-      lo = __ldcg(p.offsets + e);
-      hi = __ldcg(p.offsets + e + 1);
-      bad |= lo < 0 || hi < lo || hi > p.rows;
-      lo = min(max(lo, 0), p.rows);
-      hi = min(max(hi, lo), p.rows);
-    }
-    const int t = (hi - lo + p.bn - 1) / p.bn * p.m_tiles;
+  for (int e = lane; e < E; e += 32) {
+    const int lo = __ldcg(p.offsets + e), hi = __ldcg(p.offsets + e + 1);
+    bad |= lo < 0 || hi < lo || hi > p.rows;
+    off[e] = lo;
+    if (e == E - 1) off[E] = hi;
+  }
+  __syncwarp();
+  if (__any_sync(kFull, bad)) {  // offsets out of range: nothing is computed
+    if (lane == 0) record_error(p.status, MHC_ERR_DEVICE_INDEX);
+    for (int e = lane; e <= E; e += 32) first[e] = 0;
+    return;
+  }
+  if (order != nullptr) {  // by falling rows of a tile, experts without rows last
+    int n = 0;
+    for (int c = p.bn / 32; c >= 0; --c)
+      for (int e0 = 0; e0 < E; e0 += 32) {
+        const int e = e0 + lane;
+        const bool in = e < E && even_rows(off[min(e, E - 1) + 1] - off[min(e, E - 1)], p.bn) == 32 * c;
+        const unsigned lanes = __ballot_sync(kFull, in);
+        if (in) order[n + __popc(lanes & ((1u << lane) - 1u))] = e;
+        n += __popc(lanes);
+      }
+    __syncwarp();
+  }
+  int run = 0;
+  for (int i0 = 0; i0 < E; i0 += 32) {
+    const int i = i0 + lane, e = i < E ? (order != nullptr ? order[i] : i) : 0;
+    const int t = i < E ? (off[e + 1] - off[e] + p.bn - 1) / p.bn * p.m_tiles : 0;
     int scan = t;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int o = __shfl_up_sync(kFull, scan, d);
       if (lane >= d) scan += o;
     }
-    if (e < p.experts) {
-      first[e] = run + scan - t;
-      off[e] = lo;
-      if (e == p.experts - 1) off[p.experts] = hi;
-    }
+    if (i < E) first[i] = run + scan - t;
     run += __shfl_sync(kFull, scan, 31);
   }
-  if (lane == 0) first[p.experts] = run;
-  if (__any_sync(kFull, bad)) {  // offsets out of range: nothing is computed
-    if (lane == 0) record_error(p.status, MHC_ERR_DEVICE_INDEX);
-    __syncwarp();
-    for (int e = lane; e <= p.experts; e += 32) first[e] = 0;
-  }
+  if (lane == 0) first[E] = run;
 }
 
-__host__ __device__ constexpr int round32(int v) { return (v + 31) / 32 * 32; }
-
-// tile_at with an expert's rows in nearly equal tiles (multiples of 32 but the last).
+// tile_at with an expert's rows in nearly equal tiles.
 template <int SRC>
-__device__ __forceinline__ TileAt tile_even(const GemmParams& p, const int* first, const int* off, int tile) {
-  TileAt t = tile_at<SRC>(p, first, off, tile);
+__device__ __forceinline__ TileAt tile_even(const GemmParams& p, const int* first, const int* off, const int* order,
+                                            int tile) {
+  TileAt t = tile_at<SRC>(p, first, off, tile, order);
   if constexpr (SRC != kDense) {
-    const int begin = off[t.expert], n = off[t.expert + 1] - begin;
-    const int tt = (n + p.bn - 1) / p.bn, each = round32((n + tt - 1) / tt);
+    const int begin = off[t.expert], each = even_rows(off[t.expert + 1] - begin, p.bn);
     t.tok0 = begin + (t.tok0 - begin) / p.bn * each;
     t.ntok = min(each, off[t.expert + 1] - t.tok0);
   }
@@ -518,7 +535,7 @@ __global__ void __launch_bounds__(kGemmThreads, CTAS)
     // they are there (and read from L2), and the second product can ask for its
     // weights while the first ends.
     if constexpr (SRC == kGather) griddep_wait();
-    if (warp == 0) expert_tiles(p, first, off, lane);
+    if (warp == 0) expert_tiles(p, first, off, nullptr, lane);
   }
   tcgen05_fence_before();
   __syncthreads();
@@ -990,7 +1007,7 @@ template <bool FP8, bool GATED, int SRC>
 mhc_status launch_pair(GemmParams& p, const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& ws,
                        const CUtensorMap& xs, cudaStream_t stream) {
   constexpr int acc = GATED ? 2 : 1;
-  const int fixed = 1024 + (SRC == kDense ? 0 : 8 * (p.experts + 1));
+  const int fixed = 1024 + (SRC == kDense ? 0 : 12 * (p.experts + 1));
   const int stage = acc * kATile + p.bn / 2 * 128 + (FP8 ? 3 * 512 : 0);
   p.stages = (kGemmSmem - kStaticSmem - fixed) / stage;
   if (p.stages > kMaxStages) p.stages = kMaxStages;

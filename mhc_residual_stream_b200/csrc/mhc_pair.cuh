@@ -118,6 +118,13 @@ __global__ void __launch_bounds__(256) permute_rows_kernel(const GemmParams p, _
   }
 }
 
+// A pair's tile of a wave. The experts' tiles come in falling size and the waves run
+// forth and back, so that the pairs' sums of sizes are nearly equal: of 16384 rows by 32
+// uneven experts the longest has 8% more than the mean, 22% in the experts' own order.
+__device__ __forceinline__ int pair_tile(int wave, int pair, int pairs) {
+  return wave * pairs + (wave & 1 ? pairs - 1 - pair : pair);
+}
+
 template <bool FP8, bool GATED, int SRC>
 __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
     pair_kernel(const __grid_constant__ GemmParams p, const __grid_constant__ CUtensorMap tm_w,
@@ -140,9 +147,11 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
   const unsigned sf0 = x0 + p.stages * x_bytes;
   int* first = nullptr;
   int* off = nullptr;
+  int* order = nullptr;
   if constexpr (SRC != kDense) {
     first = reinterpret_cast<int*>(raw + (sf0 - smem_u32(raw)));
     off = first + p.experts + 1;
+    order = off + p.experts + 1;
   }
   if (tid == 0) {
     prefetch_tensormap(&tm_w);
@@ -166,7 +175,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
   } else {
     // As in gemm_kernel: the kernel before waited for the offsets before it let this
     // one start.
-    if (warp == 0) expert_tiles(p, first, off, lane);
+    if (warp == 0) expert_tiles(p, first, off, order, lane);
   }
   tcgen05_fence_before();
   __syncthreads();
@@ -187,8 +196,8 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
     int s = 0;
     unsigned ph = 1;
     bool ok = true;
-    for (int tile = pair; ok && tile < tiles; tile += pairs) {
-      const TileAt t = tile_even<SRC>(p, first, off, tile);
+    for (int wave = 0, tile = pair; ok && tile < tiles; tile = pair_tile(++wave, pair, pairs)) {
+      const TileAt t = tile_even<SRC>(p, first, off, order, tile);
       const int half = round32(t.ntok) / 2;
       const int wrow = (SRC == kDense ? 0 : t.expert * (kAcc * p.n)) + t.m * kPairTileM + rank * kTileM;
       const int xrow = t.tok0 + rank * half;
@@ -229,8 +238,8 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
       int s = 0, buf = 0;
       unsigned ph = 0, aph = 1;
       bool ok = true;
-      for (int tile = pair; ok && tile < tiles; tile += pairs) {
-        const TileAt t = tile_even<SRC>(p, first, off, tile);
+      for (int wave = 0, tile = pair; ok && tile < tiles; tile = pair_tile(++wave, pair, pairs)) {
+        const TileAt t = tile_even<SRC>(p, first, off, order, tile);
         const unsigned idesc = p.idesc | (static_cast<unsigned>(round32(t.ntok) >> 3) << 17);
         if (!(ok = __all_sync(kFull, wait_for_cluster(&acc_empty[buf], aph, p)))) break;
         tcgen05_fence_after();
@@ -276,8 +285,8 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
     const int q = warp & 3, part = (warp - 2) >> 2;
     int buf = 0;
     unsigned ph = 0;
-    for (int tile = pair; tile < tiles; tile += pairs) {
-      const TileAt t = tile_even<SRC>(p, first, off, tile);
+    for (int wave = 0, tile = pair; tile < tiles; tile = pair_tile(++wave, pair, pairs)) {
+      const TileAt t = tile_even<SRC>(p, first, off, order, tile);
       const int f = t.m * kPairTileM + rank * kTileM + q * 32 + lane;
       float bg = 0.f, bu = 0.f;
       if (p.bias != nullptr && f < p.n) {

@@ -599,7 +599,10 @@ def mhc_linear(x, weight, out, bias=None, activation: str = "none", residual=Non
     """out [R, N] = activation(x [R, K] @ weight [N, K]^T + bias [N]) + residual [R, N].
     x and weight are bf16, or both MXFP8 as (data, scale, True); out is bf16 or fp32.
     activation: none, relu, silu, gelu, or swiglu (weight [2N, K], bias [2N]: gate rows,
-    then up rows). Rows of x, residual and out may be strided; residual may be out."""
+    then up rows). Rows of x, residual and out may be strided; residual may be out.
+    The call may read weight while the kernel before it on the stream still runs: weight
+    must not be an output of the mhc_linear, mhc_moe_experts or boundary call directly
+    before (what mxfp8_quantize_rows or another library's kernel writes there is fine)."""
     act = ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
