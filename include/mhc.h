@@ -327,11 +327,8 @@ MHC_API mhc_status mxfp8_quantize_rows(const mhc_bf16* x, int rows, int hidden,
  * expanded_idx_to_permuted_idx and gemm2_permuted ([decode] SpecializedDecode.run:
  * MoEStep; the pages name these steps and print none of their arithmetic).
  * Rows are tokens; 1 <= rows <= 65535 here (a prompt's rows too, not only a
- * decode batch's). The conventions above hold. Their rule on weights and dependent
- * launches concerns `weight` and `weight_scale` of mhc_linear, which it reads ahead
- * of its wait: they must not be an output of the mhc_linear, mhc_moe_experts or
- * boundary call launched directly before on the stream (mxfp8_quantize_rows,
- * mhc_projection_pack and kernels of other libraries may write them there).
+ * decode batch's). The conventions above hold; their rule on weights and dependent
+ * launches concerns mhc_linear's `weight` and `weight_scale` (see read_ahead).
  *
  * mhc_linear: out[r, f] = act( sum_k x[r, k] weight[f, k] + bias[f] ) + residual[r, f]
  *   x [rows, in] and weight [out, in] (contiguous) are bf16 (both scales NULL), or
@@ -348,6 +345,11 @@ MHC_API mhc_status mxfp8_quantize_rows(const mhc_bf16* x, int rows, int hidden,
  *   in_features a multiple of 8 (bf16) or 32 (MXFP8), <= 65536; out_features <=
  *   2^20, a multiple of 128 for MXFP8 with SWIGLU. x and weight 16-byte aligned,
  *   scales 16-byte aligned.
+ *   read_ahead != 0: the kernel may read weight and weight_scale before the kernel
+ *   before it on the stream has ended. They must then not be an output of the
+ *   mhc_linear, mhc_moe_experts or boundary call launched directly before (what
+ *   mxfp8_quantize_rows, mhc_projection_pack or another library's kernel writes there
+ *   is waited for). 0: every read waits, for weights that are themselves computed.
  *   workspace: mhc_linear_workspace_bytes(rows) bytes (a size for more rows serves
  *   fewer), 256-byte aligned, zeroed once before first use (mhc_workspace_init),
  *   used by one stream at a time; two graphs that may run at once need one each. A
@@ -364,7 +366,7 @@ MHC_API size_t mhc_linear_workspace_bytes(int rows);
 MHC_API mhc_status mhc_linear(
     const void* x, const uint8_t* x_scale, int64_t x_stride, const void* weight, const uint8_t* weight_scale,
     const float* bias, mhc_activation activation, const mhc_bf16* residual, int64_t residual_stride,
-    void* out, int out_fp32, int64_t out_stride, int rows, int in_features, int out_features,
+    void* out, int out_fp32, int64_t out_stride, int rows, int in_features, int out_features, int read_ahead,
     void* workspace, size_t ws_bytes, mhc_stream stream);
 
 /* mhc_moe_route: the experts of each row and the permutation of the pairs

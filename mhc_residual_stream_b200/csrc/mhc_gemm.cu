@@ -81,6 +81,7 @@ struct GemmParams {
   void* out;
   int64_t out_stride;
   int out_fp32, act;
+  int read_ahead;  // the weights are not the preceding kernel's to write
   int paired;  // bf16 output (and residual) whose rows allow 4-byte accesses
   unsigned* status;
   unsigned* counters;
@@ -578,12 +579,12 @@ __global__ void __launch_bounds__(kGemmThreads, CTAS)
     };
     int ahead = 0;  // stages whose weights were requested before the wait
     if constexpr (SRC != kGather) {
-      // The weights are not the preceding kernel's to write: the first stages'
-      // are requested before waiting for it. (More of them asked into L2 there made every
+      // The weights are not the preceding kernel's to write (p.read_ahead): the first
+      // stages' are requested before waiting for it. (More of them asked into L2 there made every
       // product slower: 32 gated rows 15.5 us, 17.0 with 8 blocks a CTA, 18.1 with 32.)
       Segments it(sched);
       Segment g;
-      while (ahead < p.stages && it.next(g)) {
+      while (p.read_ahead && ahead < p.stages && it.next(g)) {
         const TileAt t = tile_at<SRC>(p, first, off, g.tile);
         for (int kb = g.k0; kb < g.k1 && ahead < p.stages; ++kb, ++ahead)
           if (elect_one()) load_w(ahead, t, kb);
@@ -1066,8 +1067,8 @@ size_t mhc_linear_workspace_bytes(int rows) {
 mhc_status mhc_linear(const void* x, const uint8_t* x_scale, int64_t x_stride, const void* weight,
                       const uint8_t* weight_scale, const float* bias, mhc_activation activation,
                       const mhc_bf16* residual, int64_t residual_stride, void* out, int out_fp32, int64_t out_stride,
-                      int rows, int in_features, int out_features, void* workspace, size_t ws_bytes,
-                      mhc_stream stream) {
+                      int rows, int in_features, int out_features, int read_ahead, void* workspace,
+                      size_t ws_bytes, mhc_stream stream) {
   const bool fp8 = weight_scale != nullptr;
   const bool gated = activation == MHC_ACT_SWIGLU;
   if (rows < 1 || rows > kMaxTokens || in_features < 1 || in_features > kMaxK || out_features < 1 ||
@@ -1099,6 +1100,7 @@ mhc_status mhc_linear(const void* x, const uint8_t* x_scale, int64_t x_stride, c
   p.out_stride = out_stride;
   p.out_fp32 = out_fp32 != 0;
   p.act = activation;
+  p.read_ahead = read_ahead != 0;
   p.paired = !out_fp32 && aligned(out, 4) && out_stride % 2 == 0 && out_features % 2 == 0 && aligned(residual, 4) &&
              residual_stride % 2 == 0;
   p.status = static_cast<unsigned*>(workspace);
@@ -1153,6 +1155,7 @@ mhc_status mhc_moe_experts(const mhc_bf16* x, int64_t x_stride, const mhc_bf16* 
   p.x_rows = rows;
   p.experts = experts;
   p.paired = 1;
+  p.read_ahead = 1;  // of w2, while the first product ends
   p.offsets = expert_offsets;
   p.prow = permuted_rows;
   p.status = reinterpret_cast<unsigned*>(ws);

@@ -129,7 +129,7 @@ def lib() -> ctypes.CDLL:
         "mhc_projection_pack_bytes": (_sz, [_i, _i]),
         "mhc_projection_pack": (_i, [_vp, _vp, _i, _i, _vp]),
         "mhc_linear_workspace_bytes": (_sz, [_i]),
-        "mhc_linear": (_i, [_vp, _vp, _i64, _vp, _vp, _vp, _i, _vp, _i64, _vp, _i, _i64, _i, _i, _i, _vp, _sz, _vp]),
+        "mhc_linear": (_i, [_vp, _vp, _i64, _vp, _vp, _vp, _i, _vp, _i64, _vp, _i, _i64, _i, _i, _i, _i, _vp, _sz, _vp]),
         "mhc_moe_route_workspace_bytes": (_sz, [_i, _i, _i]),
         "mhc_moe_route": (_i, [_vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _vp, _sz, _vp]),
         "mhc_moe_experts_workspace_bytes": (_sz, [_i, _i, _i]),
@@ -595,14 +595,16 @@ def _operand(v, name, dev, arg):
     return data, pd, ps
 
 
-def mhc_linear(x, weight, out, bias=None, activation: str = "none", residual=None, workspace=None, stream=None):
+def mhc_linear(x, weight, out, bias=None, activation: str = "none", residual=None, workspace=None, stream=None,
+               read_ahead: bool = True):
     """out [R, N] = activation(x [R, K] @ weight [N, K]^T + bias [N]) + residual [R, N].
     x and weight are bf16, or both MXFP8 as (data, scale, True); out is bf16 or fp32.
     activation: none, relu, silu, gelu, or swiglu (weight [2N, K], bias [2N]: gate rows,
     then up rows). Rows of x, residual and out may be strided; residual may be out.
-    The call may read weight while the kernel before it on the stream still runs: weight
-    must not be an output of the mhc_linear, mhc_moe_experts or boundary call directly
-    before (what mxfp8_quantize_rows or another library's kernel writes there is fine)."""
+    With read_ahead the call may read weight while the kernel before it on the stream
+    still runs: turn it off where weight is an output of the mhc_linear, mhc_moe_experts
+    or boundary call directly before (what mxfp8_quantize_rows or another library's
+    kernel writes there is waited for)."""
     act = ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
@@ -624,7 +626,7 @@ def mhc_linear(x, weight, out, bias=None, activation: str = "none", residual=Non
         raise ValueError("x/weight/bias/residual/out shapes disagree")
     st = (_lib or lib()).mhc_linear(px, pxs, _row_stride(xd, "x"), pw, pws, pb, act, pr,
                           0 if pr is None else _row_stride(residual, "residual"), po, fp32, _row_stride(out, "out"),
-                          R, K, N, pws_, wsb, _raw_stream(stream, dev))
+                          R, K, N, read_ahead, pws_, wsb, _raw_stream(stream, dev))
     if st:
         raise MhcError(st, "mhc_linear")
 

@@ -138,6 +138,23 @@ def test_linear_takes_what_the_quantizer_writes():
     assert_within(got, exact, bound, "quantized operands")
 
 
+def test_linear_of_a_weight_that_the_call_before_computes():
+    g = gen(30)
+    a, b, x = bf((256, 4096), g, 0.02).to(DEV), bf((512, 4096), g, 0.02).to(DEV), bf((24, 512), g).to(DEV)
+    ws, w = M.new_linear_workspace(256, DEV), torch.empty(256, 512, dtype=torch.bfloat16, device=DEV)
+    outs = []
+    for _ in range(20):
+        w.zero_()
+        torch.cuda.synchronize()
+        M.mhc_linear(a, b, w, workspace=ws)
+        out = torch.empty(24, 256, dtype=torch.bfloat16, device=DEV)
+        M.mhc_linear(x, w, out, workspace=ws, read_ahead=False)
+        outs.append(out)
+    exact, bound = linear_bound(f64(x), f64(w), None, "none", None, torch.bfloat16)
+    for out in outs:
+        assert_within(out, exact, bound, "computed weight")
+
+
 def test_linear_strided_rows_and_untouched_surroundings():
     g = gen(4)
     xb, rb = bf((37, 208), g).to(DEV), bf((37, 90), g).to(DEV)

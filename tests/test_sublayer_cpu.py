@@ -29,7 +29,7 @@ def _a(addr=0x10000):
 def test_linear_refusals(L):
     a = _a()
     base = dict(x=a, xs=None, xst=64, w=a, wsc=None, bias=None, act=0, res=None, rst=0, out=a, fp32=0, ost=100, R=4, K=64,
-                N=100, ws=a, wsb=1 << 30, s=None)
+                N=100, ahead=1, ws=a, wsb=1 << 30, s=None)
 
     def call(**kw):
         return L.mhc_linear(*{**base, **kw}.values())
