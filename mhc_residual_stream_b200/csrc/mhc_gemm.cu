@@ -31,7 +31,6 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <cstring>
 
 #include "../../include/mhc.h"
 #include "mhc_device.cuh"
@@ -154,7 +153,9 @@ struct Segments {  // iterates over a CTA's segments
 };
 
 // Token columns that each CTA of a cluster of `split` finishes, in fours.
-__host__ __device__ constexpr int columns_each(int cols, int split) { return ((cols + split - 1) / split + 3) / 4 * 4; }
+__host__ __device__ constexpr int columns_each(int cols, int split) {
+  return ((cols + split - 1) / split + 3) / 4 * 4;
+}
 
 struct TileAt {
   int m, expert, tok0, ntok;
@@ -295,8 +296,12 @@ __device__ __forceinline__ bool epilogue_all(bool ok) {
 
 // Every thread of the cluster: what was written before its arrival is seen after
 // the wait. Whole warps.
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 // Of the warps that have no part in a cluster's epilogue: its two barriers but the
 // second one's wait, which ends the kernel.
 __device__ __forceinline__ void pass_cluster_barriers(bool apart) {
@@ -312,9 +317,10 @@ __device__ __forceinline__ unsigned cluster_address(unsigned addr, int rank) {
 }
 // Shared memory to the shared memory of a CTA of the cluster, counted on its barrier.
 __device__ __forceinline__ void bulk_s2cluster(unsigned dst, unsigned src, unsigned bytes, unsigned bar) {
-  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "r"(src), "r"(bytes), "r"(bar)
-               : "memory");
+  asm volatile(
+      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "r"(src), "r"(bytes), "r"(bar)
+      : "memory");
 }
 
 __device__ __forceinline__ float silu(float v) { return v / (1.f + __expf(-v)); }
@@ -581,7 +587,9 @@ __global__ void __launch_bounds__(kGemmThreads, CTAS)
     if constexpr (SRC != kGather) {
       // The weights are not the preceding kernel's to write (p.read_ahead): the first
       // stages' are requested before waiting for it. (More of them asked into L2 there made every
-      // product slower: 32 gated rows 15.5 us, 17.0 with 8 blocks a CTA, 18.1 with 32.)
+      // product slower: 32 gated rows 15.5 us, 17.0 with 8 blocks a CTA, 18.1 with 32. The
+      // gathering product, which has waited by now, is slower with its first weights asked
+      // before its row numbers: experts of 1 row 121.0 us, 122.2.)
       Segments it(sched);
       Segment g;
       while (p.read_ahead && ahead < p.stages && it.next(g)) {
@@ -731,7 +739,8 @@ __global__ void __launch_bounds__(kGemmThreads, CTAS)
       const bool whole = g.k0 == 0 && g.k1 == p.kblocks;
       const size_t slot_floats = static_cast<size_t>(kAcc) * p.bn * kTileM;
       // partial sums of a shared tile in the workspace, [column][feature]
-      float* slot = p.partials + (static_cast<size_t>(sched.cta) * 2 + (g.k0 > 0 ? 0 : 1)) * slot_floats + q * 32 + lane;
+      const size_t own = static_cast<size_t>(sched.cta) * 2 + (g.k0 > 0 ? 0 : 1);
+      float* slot = p.partials + own * slot_floats + q * 32 + lane;
       for (int c = 0; c < t.ntok; c += 16) {
         float v[16], u[16];
         read_sums<GATED>(src + c, p.bn, v, u);
@@ -770,8 +779,8 @@ __global__ void __launch_bounds__(kGemmThreads, CTAS)
 #pragma unroll
         for (int k = 0; k < kMaxShares; ++k) {
           const int o = min(c0 + k, c1);
-          from[k] = p.partials + (static_cast<size_t>(o) * 2 + (sched.start_of(o) > w0 ? 0 : 1)) * slot_floats + q * 32 +
-                    lane;
+          const size_t theirs = static_cast<size_t>(o) * 2 + (sched.start_of(o) > w0 ? 0 : 1);
+          from[k] = p.partials + theirs * slot_floats + q * 32 + lane;
         }
         const int shares = c1 - c0 + 1;
         for (int c = 0; c < t.ntok; c += 4) {
@@ -1223,7 +1232,8 @@ mhc_status mhc_moe_experts(const mhc_bf16* x, int64_t x_stride, const mhc_bf16* 
   p.act = MHC_ACT_NONE;
   if (!make_map2(&mw, w2, false, intermediate, static_cast<uint64_t>(experts) * hidden,
                  static_cast<uint64_t>(intermediate) * 2, kTileM) ||
-      !make_map2(&mx, inner, false, intermediate, num_permuted, static_cast<uint64_t>(intermediate) * 2, pair ? 16 : p.bn))
+      !make_map2(&mx, inner, false, intermediate, num_permuted, static_cast<uint64_t>(intermediate) * 2,
+                 pair ? 16 : p.bn))
     return MHC_ERR_CUDA;
   if (pair) return launch_pair<false, false, kGrouped>(p, mw, mx, mw, mx, stream);
   return launch_gemm<false, false, kGrouped, 1>(p, mw, mx, grid, 1, stream);

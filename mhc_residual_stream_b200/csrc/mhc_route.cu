@@ -151,7 +151,8 @@ __device__ unsigned keep_groups(const RouteParams& p, const double* choice, int 
 
 // The same in fp32; sets `near` where the last group that stays and the first that
 // does not are too near.
-__device__ __forceinline__ unsigned keep_groups(const RouteParams& p, const float* choice, int lane, float unit, bool* near) {
+__device__ __forceinline__ unsigned keep_groups(const RouteParams& p, const float* choice, int lane, float unit,
+                                                bool* near) {
   const int G = p.groups, S = p.group_size, per = 1 << p.lanes_log;
   const int g = lane >> p.lanes_log, sub = lane & (per - 1);
   float v1 = -INFINITY, v2 = -INFINITY;
@@ -619,7 +620,8 @@ mhc_status run(RouteParams& p, cudaStream_t stream) {
   static std::atomic<int> c_fused[64], c_choose[64];
   static std::atomic<int> c_place[64];
   // a row's choices, in 64 bits where the fp32 ones decide nothing
-  const size_t count = (p.E * 4 + 15) & ~15, choice = p.bias != nullptr || p.groups > 1 ? static_cast<size_t>(p.E) * 8 : 0;
+  const size_t count = (p.E * 4 + 15) & ~15;
+  const size_t choice = p.bias != nullptr || p.groups > 1 ? static_cast<size_t>(p.E) * 8 : 0;
   if (p.rows <= kClusterRows) {
     const size_t choose = count + kFewWarps * choice, place = static_cast<size_t>(kFewWarps + 2) * p.E * 4;
     p.blocks = (p.rows + kFewWarps - 1) / kFewWarps;
