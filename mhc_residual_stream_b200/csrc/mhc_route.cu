@@ -99,14 +99,13 @@ __device__ __forceinline__ double warp_sum(double v) {
 // The groups of the top_groups largest values: bit g << lanes_log for group g, whose
 // value (key; 0: no expert is available) the lane of that number holds.
 template <typename Key>
-__device__ __forceinline__ unsigned best_groups(const RouteParams& p, Key value, int lane, int* rank_out) {
+__device__ __forceinline__ unsigned best_groups(const RouteParams& p, Key value, int lane) {
   const int G = p.groups, g = lane >> p.lanes_log;
   int rank = 0;  // groups ahead of this lane's
   for (int o = 0; o < G; ++o) {
     const Key w = __shfl_sync(kFull, value, o << p.lanes_log);
     rank += w > value || (w == value && o < g) ? 1 : 0;
   }
-  *rank_out = rank;
   return __ballot_sync(kFull, g < G && rank < p.top_groups && value != 0);
 }
 
@@ -145,12 +144,15 @@ __device__ unsigned keep_groups(const RouteParams& p, const double* choice, int 
     take(o2, w2);
   }
   const uint64_t value = k1 == 0 ? 0 : order_key(p.group_top == 2 && k2 != 0 ? v1 + v2 : v1);
-  int rank;
-  return best_groups(p, static_cast<unsigned long long>(value), lane, &rank);
+  return best_groups(p, static_cast<unsigned long long>(value), lane);
 }
 
-// The same in fp32; sets `near` where the last group that stays and the first that
-// does not are too near.
+// The same in fp32; sets `near` where the groups that stay and those that do not cannot be
+// told apart: where the least that one of the first may be worth does not exceed the most
+// that one of the others may be. Each group has an error of its own (two choices of
+// opposite sign may cancel, and leave a small value with their rounding), so a group of any
+// rank counts. Three warp-wide maxima (8191 rows x 200 experts in 8 groups 25.0 us, as with
+// only the two groups at the border compared, which kept wrong groups).
 __device__ __forceinline__ unsigned keep_groups(const RouteParams& p, const float* choice, int lane, float unit,
                                                 bool* near) {
   const int G = p.groups, S = p.group_size, per = 1 << p.lanes_log;
@@ -169,15 +171,19 @@ __device__ __forceinline__ unsigned keep_groups(const RouteParams& p, const floa
   }
   const bool two = p.group_top == 2 && v2 > -INFINITY;
   const float value = two ? v1 + v2 : v1;
-  const float mag = two ? fabsf(v1) + fabsf(v2) + fabsf(value) : fabsf(v1);  // two choices of opposite sign may cancel
-  int rank;
-  const unsigned mask = best_groups(p, order_key(value), lane, &rank);
+  const unsigned mask = best_groups(p, order_key(value), lane);
   if (p.top_groups < G) {
-    const unsigned in = __ballot_sync(kFull, g < G && sub == 0 && rank == p.top_groups - 1);
-    const unsigned out = __ballot_sync(kFull, g < G && sub == 0 && rank == p.top_groups);
-    const float a = __shfl_sync(kFull, value, __ffs(in) - 1), b = __shfl_sync(kFull, value, __ffs(out) - 1);
-    const float ma = __shfl_sync(kFull, mag, __ffs(in) - 1), mb = __shfl_sync(kFull, mag, __ffs(out) - 1);
-    *near = b > -INFINITY && too_near(a, b, 4.f * unit, ma + mb);
+    const bool open = v1 > -INFINITY;  // the group has an expert that can be chosen
+    const bool stays = mask >> (g << p.lanes_log) & 1u;
+    // Values as their distances from the last group that stays, which are exact where they
+    // are small. Their errors: those of the choices (see too_near), a rounding of the sum,
+    // and what a larger distance and its bound are rounded by.
+    const float d = value + warp_max(open && stays ? -value : -INFINITY);
+    const float err = 0x1p-24f * (2.f * unit + fabsf(v1) + (two ? fabsf(v2) + fabsf(value) : 0.f) + 2.f * fabsf(d));
+    const float least = -warp_max(open && stays ? err - d : -INFINITY);
+    const float most = warp_max(open && !stays ? d + err : -INFINITY);
+    // a value outside fp32's range compares with nothing
+    *near = !(least > most) || __any_sync(kFull, open && !(fabsf(value) < INFINITY));
   }
   return mask;
 }

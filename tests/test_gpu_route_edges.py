@@ -1,0 +1,59 @@
+"""GPU tests of mhc_moe_route where its fp32 choices and the 64-bit definition part:
+groups whose values carry unlike errors or leave fp32's range, scores below it."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from mhc_residual_stream_b200 import mhc as M
+
+from _sublayer import DEV, f64, gen, run_route
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from mhc_residual_stream_b200 import build
+    build.build()
+    M.lib()
+    yield
+
+
+def ids_agree(logits, k, bias, **kw):
+    got = run_route(logits.to(DEV), k, bias.to(DEV), **kw)
+    w, ids, e2p, prow, off = [t.cpu() for t in got]
+    ow, oids = O.moe_route(f64(logits), k, f64(bias), **kw)
+    wrong = (ids.numpy() != oids).any(1)
+    assert not wrong.any(), f"{wrong.sum()} of {len(wrong)} rows, the first is {np.argwhere(wrong)[0, 0]}"
+    for a, b in zip((e2p, prow, off), O.moe_permute(oids, logits.shape[1])):
+        assert np.array_equal(a.numpy(), b)
+    return f64(w), ow
+
+
+@pytest.mark.parametrize("top_groups", [1, 2, 3])
+@pytest.mark.parametrize("size", [32.0, 128.0, 1000.0])
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+def test_a_group_that_cancels_among_groups_that_do_not(scoring, size, top_groups):
+    # four nearly equal groups, one of them the sum of +size and -size: its value in fp32 is
+    # off by a step of `size`, the others' by a step of one, and it may stand at any rank
+    R, G, S = 1500, 4, 2
+    for cancels in (0, 3):
+        logits = 1.0 + 1e-5 * torch.randn(R, G * S, generator=gen(int(size) + cancels))
+        bias = torch.zeros(G * S)
+        bias[cancels * S], bias[cancels * S + 1] = size, -size
+        ids_agree(logits, 2, bias, scoring=scoring, num_groups=G, top_groups=top_groups, group_top=2)
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_group_values_outside_the_range_of_fp32(sign):
+    R, G, S = 20, 4, 3
+    logits = torch.randn(R, G * S, generator=gen(3))
+    bias = sign * torch.tensor([3.0e38, 3.2e38, 2.8e38, 3.1e38]).repeat_interleave(S)
+    for tg in (1, 2, 3):
+        ids_agree(logits, 3, bias, scoring="sigmoid", num_groups=G, top_groups=tg, group_top=2)
+    bias[:S] = 0.0  # one group within it
+    ids_agree(logits, 3, bias, scoring="sigmoid", num_groups=G, top_groups=2, group_top=2)
