@@ -421,8 +421,10 @@ __device__ __forceinline__ void choose_row(const RouteParams& p, int row, int la
   if (p.renorm) {
     float total = warp_sum(w);
     if (!p.softmax && total < 1e-20f) {
-      // every chosen sigmoid is near or below fp32's range: the ratio in 64 bits
-      double d = id >= 0 ? 1.0 / (1.0 + exp(-static_cast<double>(chosen))) : 0.0;
+      // every chosen sigmoid is near or below fp32's range: the ratio in 64 bits, where
+      // the sigmoid of less than -46 is the exponential (1 + e^46 is e^46 to 2^-66), which
+      // unlike 1 / e^-l reaches the subnormals
+      const double d = id >= 0 ? exp(static_cast<double>(chosen)) : 0.0;
       const double all = warp_sum(d);
       w = all > 0.0 ? static_cast<float>(d / all) : 0.f;
     } else {

@@ -57,3 +57,21 @@ def test_group_values_outside_the_range_of_fp32(sign):
         ids_agree(logits, 3, bias, scoring="sigmoid", num_groups=G, top_groups=tg, group_top=2)
     bias[:S] = 0.0  # one group within it
     ids_agree(logits, 3, bias, scoring="sigmoid", num_groups=G, top_groups=2, group_top=2)
+
+
+def test_weights_of_scores_that_only_subnormals_hold():
+    # sigmoid scores of exp(-735) .. exp(-705): below exp(-708) subnormal in 64 bits, 2^-1074
+    # apart, and 1 / (1 + exp(-l)) is 0 there although the score is not
+    R, E, k = 40, 12, 4
+    logits = -705.0 - 30.0 * torch.rand(R, E, generator=gen(5))
+    got = run_route(logits.to(DEV), k, scoring="sigmoid")
+    ow, oids = O.moe_route(f64(logits), k, scoring="sigmoid")
+    w, ids = f64(got[0]), got[1].cpu().numpy()
+    assert np.array_equal(ids, oids)
+    chosen = np.take_along_axis(f64(logits), oids, 1)
+    exact = np.exp(chosen - chosen.max(1, keepdims=True))
+    exact /= exact.sum(1, keepdims=True)
+    spacing = 2.0 ** -1074 / np.exp(chosen.max(1, keepdims=True))  # of a score, relative to the largest
+    # each score is off by half a spacing at most, the sum by k of them; one rounding to fp32
+    assert np.all(np.abs(w - exact) <= (k + 1) * spacing + 2.0 ** -23 * exact + 2.0 ** -126)
+    assert np.all(np.abs(ow - exact) <= (k + 1) * spacing + 2.0 ** -40)
