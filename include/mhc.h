@@ -353,7 +353,9 @@ MHC_API mhc_status mxfp8_quantize_rows(const mhc_bf16* x, int rows, int hidden,
  *   workspace: mhc_linear_workspace_bytes(rows) bytes (a size for more rows serves
  *   fewer), 256-byte aligned, zeroed once before first use (mhc_workspace_init),
  *   used by one stream at a time; two graphs that may run at once need one each. A
- *   workspace whose call recorded a device error is zeroed again before reuse. */
+ *   workspace whose call recorded a device error is zeroed again before reuse. One
+ *   workspace may serve this library's operators in turn, with the bytes of the one
+ *   that needs most. */
 typedef enum {
   MHC_ACT_NONE = 0,
   MHC_ACT_RELU = 1,

@@ -51,10 +51,13 @@ constexpr int kMaxExperts = 1024;
 constexpr int kMaxShares = 5;        // CTAs that share a grouped tile: up to 4 shares' worth, unaligned
 constexpr int kMinShare = 24;        // K blocks
 constexpr int kATile = kTileM * 128;  // bytes of a weight tile in a stage
-// Workspace: the status word at byte 0, the join counters at 1024, the partial
-// sums at 2048.
-constexpr size_t kGemmCounters = 1024;
+// Workspace: the status word at byte 0, the join counters at 256, the partial sums at
+// 2048. The counters must be zero when a call begins, and a call leaves them so: they lie in
+// the header, which no other operator writes behind its status word, so that one
+// workspace may serve several operators.
+constexpr size_t kGemmCounters = 256;
 constexpr size_t kGemmHeader = 2048;
+static_assert(kGemmCounters + kMaxGrid * sizeof(unsigned) <= kWsHeader, "the counters lie in the header");
 
 enum Source { kDense = 0, kGather = 1, kGrouped = 2 };
 
