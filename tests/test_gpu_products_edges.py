@@ -55,3 +55,35 @@ def test_one_workspace_serves_every_operator_in_turn():
                                 workspace=ws)
         assert torch.equal(run_experts(*ops, ws), want)
         assert M.mhc_get_device_status(ws) == M.OK
+
+
+def shares_of(tiles, kblocks, grid=148, most=4, least=24):
+    """CTAs that compute each tile behind the full waves, as the schedule divides them."""
+    rest = tiles % grid
+    total = rest * kblocks
+    parts = min(grid, rest * most, max(rest, total // least))
+
+    def owner(w):
+        return ((w + 1) * parts - 1) // total
+    return {owner((t + 1) * kblocks - 1) - owner(t * kblocks) + 1 for t in range(rest)}
+
+
+# one expert: hidden, intermediate, then the shares of a tile in the first and the second product
+SHARED = [(7168, 2048, {4}, {2, 3}), (4096, 2048, {3, 4}, {2, 3}), (6016, 4864, {4, 5}, {4, 5}),
+          (4864, 6016, {4, 5}, {4, 5}), (1152, 2560, {1}, {2, 3})]
+
+
+@pytest.mark.parametrize("H,I,first,second", SHARED)
+@pytest.mark.parametrize("R", [1, 13])
+def test_experts_tiles_of_several_shares(H, I, first, second, R):
+    got = shares_of(-(-I // 128), -(-H // 64)), shares_of(-(-H // 128), -(-I // 64))
+    assert got == (first, second)
+    x, w13, w2, e2p, prow, off = draw_experts(R, 1, 1, H, I, seed=H + R)
+    exact, bound = experts_bound(f64(x), f64(w13), f64(w2), prow, off)
+    ws = M.new_moe_experts_workspace(R, R, I, DEV)
+    ops = x.to(DEV), w13.to(DEV), w2.to(DEV), i32(prow), i32(off)
+    out = run_experts(*ops, ws)
+    assert_within(out, exact, bound, f"{R} rows, {H} x {I}")
+    for _ in range(5):
+        assert torch.equal(run_experts(*ops, ws), out)
+    assert M.mhc_get_device_status(ws) == M.OK
