@@ -48,6 +48,7 @@ constexpr int kStaticSmem = 1024;    // the barriers
 constexpr int kHalfSmem = 112 * 1024;
 constexpr int kMaxGrid = 160;        // CTAs the workspace has room for
 constexpr int kMaxExperts = 1024;
+constexpr int64_t kMinBudgetNs = 100000;  // least time limit of a bounded wait
 constexpr int kMaxShares = 5;        // CTAs that share a grouped tile: up to 4 shares' worth, unaligned
 constexpr int kMinShare = 24;        // K blocks
 constexpr int kATile = kTileM * 128;  // bytes of a weight tile in a stage
@@ -270,10 +271,12 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, unsigned parity, const G
   return false;
 }
 
-// A bounded wait on a barrier that other CTAs of the cluster arrive on.
-__device__ __forceinline__ bool wait_for_cluster(uint64_t* bar, unsigned parity, const GemmParams& p) {
+// A bounded wait on a barrier that other CTAs of the cluster arrive on, `more_ns` longer
+// than the others.
+__device__ __forceinline__ bool wait_for_cluster(uint64_t* bar, unsigned parity, const GemmParams& p,
+                                                 int64_t more_ns = 0) {
   if (mbar_try_wait_cluster(bar, parity)) return true;
-  const long long deadline = wait_deadline(p.budget_ns);
+  const long long deadline = wait_deadline(p.budget_ns + more_ns);
   while (!mbar_try_wait_cluster(bar, parity))
     if (clock64() > deadline) {
       record_error(p.status, MHC_ERR_DEVICE_TIMEOUT);
@@ -295,6 +298,15 @@ __device__ __forceinline__ bool epilogue_all(bool ok) {
       : "r"(ok ? 1u : 0u), "n"(kThreads)
       : "memory");
   return r != 0;
+}
+
+// No copy into the ring is left in flight when the CTA ends: a role that gave up waits
+// (bounded) for the ring's uses first..last-1, in the order of their requests. The copying
+// warp waits for those that it requested last, the issuing one for those it did not come to.
+__device__ __forceinline__ void drain_ring(uint64_t* full, int stages, int first, int last, const GemmParams& p) {
+  const long long deadline = wait_deadline(p.budget_ns);
+  for (int i = max(first, 0); i < last; ++i)
+    mbar_wait_bounded(&full[i % stages], static_cast<unsigned>(i / stages) & 1u, deadline);
 }
 
 // Every thread of the cluster: what was written before its arrival is seen after
@@ -423,7 +435,9 @@ __device__ __forceinline__ void add4(float (&v)[4], const float4 a) {
 // first part of its drained ring, [CTA][gate, up][column / 4][feature][4], and one
 // bulk copy per CTA takes them to that CTA: to memory of their own beside the ring, or
 // to the second part of its ring once all rings are drained; the columns that arrive
-// are added in CTA order, which is K order.
+// are added in CTA order, which is K order. A CTA whose products did not come sends NaN:
+// every CTA that finishes columns then gets all its bytes and waits for them, so that no
+// CTA of the cluster ends while a copy still reads or writes its shared memory.
 template <bool GATED>
 __device__ __forceinline__ void finish_in_cluster(const GemmParams& p, const Schedule& sched, unsigned char* raw,
                                                   unsigned smem0, unsigned tmem, unsigned ring_bytes,
@@ -447,34 +461,39 @@ __device__ __forceinline__ void finish_in_cluster(const GemmParams& p, const Sch
   const bool ok = epilogue_all(wait_for(&acc_full[0], 0, p));
   __syncwarp();
   if (!p.apart) cluster_arrive();  // this CTA's ring is drained
-  if (ok) {
-    tcgen05_fence_after();
-    const unsigned src = tmem + (static_cast<unsigned>(q * 32) << 16);
-    int at = 0;
-    unsigned to = 0;  // offset of the CTA's block
-    for (int c = 0; c < t.ntok; c += 16) {
-      float v[16], u[16];
-      read_sums<GATED>(src + c, p.bn, v, u);
+  tcgen05_fence_after();
+  const unsigned src = tmem + (static_cast<unsigned>(q * 32) << 16);
+  int at = 0;
+  unsigned to = 0;  // offset of the CTA's block
+  for (int c = 0; c < t.ntok; c += 16) {
+    float v[16], u[16];
+    read_sums<GATED>(src + c, p.bn, v, u);
+    if (!ok) {
 #pragma unroll
-      for (int i = 0; i < 16; i += 4)
-        if (c + i < t.ntok) {
-          *reinterpret_cast<float4*>(out + to + at * (kTileM * 4)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-          if constexpr (GATED)
-            *reinterpret_cast<float4*>(out + to + (each + at) * (kTileM * 4)) =
-                make_float4(u[i], u[i + 1], u[i + 2], u[i + 3]);
-          if ((at += 4) == each) {
-            at = 0;
-            to += block;
-          }
-        }
+      for (int i = 0; i < 16; ++i) v[i] = u[i] = __int_as_float(0x7fffffff);
     }
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    epilogue_barrier();
+#pragma unroll
+    for (int i = 0; i < 16; i += 4)
+      if (c + i < t.ntok) {
+        *reinterpret_cast<float4*>(out + to + at * (kTileM * 4)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        if constexpr (GATED)
+          *reinterpret_cast<float4*>(out + to + (each + at) * (kTileM * 4)) =
+              make_float4(u[i], u[i + 1], u[i + 2], u[i + 3]);
+        if ((at += 4) == each) {
+          at = 0;
+          to += block;
+        }
+      }
   }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  epilogue_barrier();
   cluster_wait();
-  if (ok && q == 2 && lane < owners) bulk_s2cluster(dst, smem0 + lane * block, block, bar);
+  if (q == 2 && lane < owners) bulk_s2cluster(dst, smem0 + lane * block, block, bar);
   __syncwarp();
-  if (ok && n > 0 && __all_sync(kFull, wait_for_cluster(sums_in, 0, p))) {
+  // A CTA sends at the latest when its own wait has run out, and that began no later than
+  // this one: twice the limit, and the copies' own time, are enough in every case.
+  const bool got = n > 0 && __all_sync(kFull, wait_for_cluster(sums_in, 0, p, p.budget_ns + kMinBudgetNs));
+  if (got && ok) {
     const float4* from = reinterpret_cast<const float4*>(raw + (sums0 - smem_u32(raw))) + row;
     for (int c = 0; c < n; c += 4) {
       float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
@@ -653,13 +672,7 @@ __global__ void __launch_bounds__(kGemmThreads, CTAS)
         }
       }
     }
-    if (!ok) {  // leave no copy in flight behind: wait (bounded) for the requested stages
-      const long long deadline = wait_deadline(p.budget_ns);
-      for (int q = 0; q < p.stages && q < i; ++q) {
-        const unsigned n = static_cast<unsigned>((i - 1 - q) / p.stages);  // uses of stage q completed or in flight
-        mbar_wait_bounded(&full[q], n & 1u, deadline);
-      }
-    }
+    if (!ok) drain_ring(full, p.stages, i - p.stages, i, p);
     __syncwarp();
     if (clustered) pass_cluster_barriers(p.apart);
   } else if (warp == 1) {
@@ -669,14 +682,14 @@ __global__ void __launch_bounds__(kGemmThreads, CTAS)
     const unsigned a_lo = desc_lo(smem0), b_lo = desc_lo(x0), idesc = p.idesc;
     Segments it(sched);
     Segment g;
-    int s = 0, buf = 0;
+    int i = 0, s = 0, buf = 0;
     unsigned ph = 0, aph = 1;
     bool ok = true;
     while (ok && it.next(g)) {
       if (!(ok = __all_sync(kFull, wait_for(&acc_empty[buf], aph, p)))) break;
       tcgen05_fence_after();
       const unsigned d = tmem + buf * acc_cols;
-      for (int kb = g.k0; kb < g.k1; ++kb) {
+      for (int kb = g.k0; kb < g.k1; ++kb, ++i) {
         if (!(ok = __all_sync(kFull, wait_for(&full[s], ph, p)))) break;
         tcgen05_fence_after();
         if (elect_one()) {
@@ -716,6 +729,7 @@ __global__ void __launch_bounds__(kGemmThreads, CTAS)
         aph ^= 1;
       }
     }
+    if (!ok) drain_ring(full, p.stages, i, i + p.stages, p);
     __syncwarp();
     if (clustered) pass_cluster_barriers(p.apart);
   } else {
@@ -865,6 +879,10 @@ bool make_scale_map(CUtensorMap* m, const void* base, uint64_t tiles) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// mhc_debug_set_wait's limit, but no less than what leaves the copies and products issued
+// before a wait, which take microseconds, the time to end before it gives up.
+int64_t wait_budget() { return g_budget_ns > kMinBudgetNs ? g_budget_ns : kMinBudgetNs; }
+
 // Bytes of a CTA's sums as it lays them out for its cluster, and of those it receives.
 int sums_bytes(int bn, int acc, int split) { return columns_each(bn, split) * split * acc * kTileM * 4; }
 
@@ -899,7 +917,7 @@ mhc_status launch_gemm(GemmParams& p, const CUtensorMap& w, const CUtensorMap& x
   if (p.stages < 2 || p.tmem_cols > 512 / CTAS) return MHC_ERR_UNSUPPORTED_SHAPE;
   p.idesc = (static_cast<unsigned>(p.bn >> 3) << 17) | (static_cast<unsigned>(kTileM >> 4) << 24) |
             (FP8 ? (1u << 23) : (1u << 4) | (1u << 7) | (1u << 10));
-  p.budget_ns = g_budget_ns;
+  p.budget_ns = wait_budget();
   p.extra_tx = static_cast<unsigned>(g_extra_tx) * 16;
   auto kern = gemm_kernel<FP8, GATED, SRC, CTAS>;
   static std::atomic<int> configured[64];
@@ -1029,7 +1047,7 @@ mhc_status launch_pair(GemmParams& p, const CUtensorMap& w, const CUtensorMap& x
   if (p.stages < 2 || p.bn % 32 != 0 || acc * p.bn + scale_cols > 512) return MHC_ERR_UNSUPPORTED_SHAPE;
   p.m_tiles = (p.n + kPairTileM - 1) / kPairTileM;
   p.idesc = (static_cast<unsigned>(kPairTileM >> 4) << 24) | (FP8 ? 1u << 23 : (1u << 4) | (1u << 7) | (1u << 10));
-  p.budget_ns = g_budget_ns;
+  p.budget_ns = wait_budget();
   p.extra_tx = static_cast<unsigned>(g_extra_tx) * 16;
   auto kern = pair_kernel<FP8, GATED, SRC>;
   static std::atomic<int> configured[64];

@@ -193,7 +193,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
     const unsigned bar0 = cluster_address(smem_u32(&full[0]), 0);
     griddep_wait();
     griddep_launch_dependents();
-    int s = 0;
+    int i = 0, s = 0;
     unsigned ph = 1;
     bool ok = true;
     for (int wave = 0, tile = pair; ok && tile < tiles; tile = pair_tile(++wave, pair, pairs)) {
@@ -202,7 +202,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
       const int wrow = (SRC == kDense ? 0 : t.expert * (kAcc * p.n)) + t.m * kPairTileM + rank * kTileM;
       const int xrow = t.tok0 + rank * half;
       const unsigned bytes = kAcc * kATile + (SRC == kDense ? x_bytes : half * 128) + kScales;
-      for (int kb = 0; kb < p.kblocks; ++kb) {
+      for (int kb = 0; kb < p.kblocks; ++kb, ++i) {
         if (!(ok = __all_sync(kFull, wait_for_cluster(&empty[s], ph, p)))) break;
         if (elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * bytes + p.extra_tx);
@@ -226,16 +226,17 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
         }
       }
     }
-    if (!ok) {  // leave no copy in flight behind
-      const long long until = clock64() + 200000;
-      while (clock64() < until) __nanosleep(1000);
-    }
+    // Both CTAs' copies are counted on the first one's barriers, and the pair ends together.
+    // Not counted are stages that the second CTA requests after the first has given up: the
+    // products then wait for a stage that the first did not request, for at least
+    // kMinBudgetNs from when the second's last request became possible.
+    if (!ok && rank == 0) drain_ring(full, p.stages, i - p.stages, i, p);
   } else if (warp == 1) {
     // ------------------------------------------------ products
     griddep_wait();  // as in gemm_kernel, before the first bounded wait
     if (rank == 0) {
       const unsigned a_lo = desc_lo(smem0), b_lo = desc_lo(x0);
-      int s = 0, buf = 0;
+      int i = 0, s = 0, buf = 0;
       unsigned ph = 0, aph = 1;
       bool ok = true;
       for (int wave = 0, tile = pair; ok && tile < tiles; tile = pair_tile(++wave, pair, pairs)) {
@@ -244,7 +245,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
         if (!(ok = __all_sync(kFull, wait_for_cluster(&acc_empty[buf], aph, p)))) break;
         tcgen05_fence_after();
         const unsigned d = tmem + buf * acc_cols;
-        for (int kb = 0; kb < p.kblocks; ++kb) {
+        for (int kb = 0; kb < p.kblocks; ++kb, ++i) {
           if (!(ok = __all_sync(kFull, wait_for_cluster(&full[s], ph, p)))) break;
           tcgen05_fence_after();
           if (elect_one()) {
@@ -278,6 +279,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1)
           aph ^= 1;
         }
       }
+      if (!ok) drain_ring(full, p.stages, i, i + p.stages, p);
     }
   } else {
     // ------------------------------------------------ epilogue

@@ -87,3 +87,41 @@ def test_experts_tiles_of_several_shares(H, I, first, second, R):
     for _ in range(5):
         assert torch.equal(run_experts(*ops, ws), out)
     assert M.mhc_get_device_status(ws) == M.OK
+
+
+@pytest.mark.parametrize("fp8,act,R,K,N", [
+    (False, "none", 1, 768, 1), (False, "none", 3, 7168, 256), (False, "none", 20, 7168, 256),
+    (False, "swiglu", 2, 7168, 2048), (False, "swiglu", 32, 7168, 2048), (True, "none", 4, 7168, 7168),
+    (True, "none", 64, 7168, 7168), (False, "none", 130, 128, 300), (True, "none", 700, 256, 300),
+])
+@pytest.mark.parametrize("budget", [1_000, 1_500_000])
+def test_waits_that_run_out_leave_nothing_in_flight(fp8, act, R, K, N, budget):
+    # clusters in which one CTA finishes every column (up to 4 rows) or all of them do, pairs of
+    # few K blocks: the copies are expected to bring more than they do, so every wait runs out;
+    # what follows directly, in the same shared memory, is right
+    g = gen(R + K)
+    W = 2 * N if act == "swiglu" else N
+    x, w = bf((R, K), g).to(DEV), bf((W, K), g, 0.05).to(DEV)
+    if fp8:
+        ops = []
+        for t in (x, w):
+            q = torch.empty(t.shape, dtype=torch.uint8, device=DEV)
+            s = torch.empty(M.mhc_mxfp8_scale_bytes(*t.shape, True), dtype=torch.uint8, device=DEV)
+            M.mxfp8_quantize_rows(t, q, s, True)
+            ops.append((q, s, True))
+        x, w = ops
+    want = run_linear(x, w, act=act)
+    bad, good = M.new_linear_workspace(R, DEV), M.new_linear_workspace(R, DEV)
+    out = [torch.zeros_like(want) for _ in range(6)]
+    torch.cuda.synchronize()
+    for k in range(0, 6, 2):
+        old = M.mhc_debug_set_wait(budget, 4)
+        try:
+            M.mhc_linear(x, w, out[k], activation=act, workspace=bad)
+        finally:
+            M.mhc_debug_set_wait(old, 0)
+        M.mhc_linear(x, w, out[k + 1], activation=act, workspace=good)
+    assert M.mhc_get_device_status(bad) == M.DEVICE_TIMEOUT
+    assert M.mhc_get_device_status(good) == M.OK
+    for k in (1, 3, 5):
+        assert torch.equal(out[k], want)
