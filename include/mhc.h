@@ -30,9 +30,10 @@
  *     stream is finishing, and reads the weights (fn, scale, base, norm_weight)
  *     before waiting for that kernel. So weights must not be written by the
  *     kernel launched immediately before on the same stream if that kernel
- *     triggers dependent launches (no kernel of this library writes weights;
- *     kernels that do not trigger, like ordinary library kernels, are waited
- *     for in full; mxfp8_quantize_rows does not trigger). Activations are read only after the wait.
+ *     triggers dependent launches before it ends, whichever library it is of.
+ *     (Of this library, mxfp8_quantize_rows and mhc_projection_pack do not; the
+ *     boundary, route, experts and linear calls do. A kernel that does not
+ *     trigger has ended by then.) Activations are read only after the wait.
  *   - Errors are returned, never raised or aborted on. Errors found by a kernel
  *     (a wait that ran out, a gather index out of range) are recorded in the
  *     workspace and read with mhc_get_device_status.
@@ -346,10 +347,10 @@ MHC_API mhc_status mxfp8_quantize_rows(const mhc_bf16* x, int rows, int hidden,
  *   2^20, a multiple of 128 for MXFP8 with SWIGLU. x and weight 16-byte aligned,
  *   scales 16-byte aligned.
  *   read_ahead != 0: the kernel may read weight and weight_scale before the kernel
- *   before it on the stream has ended. They must then not be an output of the
- *   mhc_linear, mhc_moe_experts or boundary call launched directly before (what
- *   mxfp8_quantize_rows, mhc_projection_pack or another library's kernel writes there
- *   is waited for). 0: every read waits, for weights that are themselves computed.
+ *   before it on the stream has ended. They must then not be an output of the kernel
+ *   launched directly before if that kernel triggers dependent launches before it ends,
+ *   of this library (see the conventions above) or of any other: it is not waited for.
+ *   0: every read waits, for weights that are themselves computed on the stream.
  *   workspace: mhc_linear_workspace_bytes(rows) bytes (a size for more rows serves
  *   fewer), 256-byte aligned, zeroed once before first use (mhc_workspace_init),
  *   used by one stream at a time; two graphs that may run at once need one each. A

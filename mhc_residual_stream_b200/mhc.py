@@ -602,9 +602,9 @@ def mhc_linear(x, weight, out, bias=None, activation: str = "none", residual=Non
     activation: none, relu, silu, gelu, or swiglu (weight [2N, K], bias [2N]: gate rows,
     then up rows). Rows of x, residual and out may be strided; residual may be out.
     With read_ahead the call may read weight while the kernel before it on the stream
-    still runs: turn it off where weight is an output of the mhc_linear, mhc_moe_experts
-    or boundary call directly before (what mxfp8_quantize_rows or another library's
-    kernel writes there is waited for)."""
+    still runs, if that kernel triggers dependent launches before it ends (of this library
+    all but mxfp8_quantize_rows and mhc_projection_pack; of another library any may). Turn
+    it off where weight is computed on the stream directly before."""
     act = ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
