@@ -478,6 +478,13 @@ MHC_API const char* mhc_status_string(mhc_status status);
  * this process. Returns the previous budget. */
 MHC_API int64_t mhc_debug_set_wait(int64_t budget_ns, int extra_units);
 
+/* Test hook: the form in which mhc_linear computes a product of these sizes on the
+ * current device (MXFP8 operands with mxfp8 != 0, SWIGLU with gated != 0), form[4]
+ * on the host: 1 for pairs of CTAs on one tile, else 0; the CTAs that divide a
+ * tile's K (1: none); CTAs per SM; token columns of a tile. Launches nothing. */
+MHC_API mhc_status mhc_debug_linear_form(int rows, int in_features, int out_features, int mxfp8, int gated,
+                                         int* form);
+
 #ifdef __cplusplus
 }
 #endif

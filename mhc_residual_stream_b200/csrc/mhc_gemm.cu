@@ -1085,9 +1085,35 @@ mhc_status launch_linear(GemmParams& p, const Plan& plan, const CUtensorMap& w, 
                           : launch_gemm<FP8, GATED, kDense, 1>(p, w, x, plan.grid, plan.split, stream);
 }
 
+bool linear_shape(int rows, int in_features, int out_features, bool fp8, bool gated) {
+  return rows >= 1 && rows <= kMaxTokens && in_features >= 1 && in_features <= kMaxK && out_features >= 1 &&
+         out_features <= kMaxFeatures && in_features % (fp8 ? 32 : 8) == 0 &&
+         !(fp8 && gated && out_features % kTileM != 0);
+}
+
+GemmParams linear_sizes(int rows, int in_features, int out_features, bool fp8) {
+  GemmParams p{};
+  p.rows = rows;
+  p.n = out_features;
+  p.kblocks = fp8 ? (in_features + 127) / 128 : (in_features + 63) / 64;
+  p.m_tiles = (out_features + kTileM - 1) / kTileM;
+  return p;
+}
+
 }  // namespace
 
 extern "C" {
+
+mhc_status mhc_debug_linear_form(int rows, int in_features, int out_features, int mxfp8, int gated, int* form) {
+  if (!form) return MHC_ERR_INVALID_ARG;
+  if (!linear_shape(rows, in_features, out_features, mxfp8 != 0, gated != 0)) return MHC_ERR_UNSUPPORTED_SHAPE;
+  const Plan plan = plan_linear(linear_sizes(rows, in_features, out_features, mxfp8 != 0), rows, mxfp8 != 0, gated != 0);
+  form[0] = plan.pair;
+  form[1] = plan.split;
+  form[2] = plan.per_sm;
+  form[3] = plan.bn;
+  return MHC_OK;
+}
 
 size_t mhc_linear_workspace_bytes(int rows) {
   if (rows < 1 || rows > kMaxTokens) return 0;
@@ -1101,9 +1127,7 @@ mhc_status mhc_linear(const void* x, const uint8_t* x_scale, int64_t x_stride, c
                       size_t ws_bytes, mhc_stream stream) {
   const bool fp8 = weight_scale != nullptr;
   const bool gated = activation == MHC_ACT_SWIGLU;
-  if (rows < 1 || rows > kMaxTokens || in_features < 1 || in_features > kMaxK || out_features < 1 ||
-      out_features > kMaxFeatures || in_features % (fp8 ? 32 : 8) != 0 || (fp8 && gated && out_features % kTileM != 0))
-    return MHC_ERR_UNSUPPORTED_SHAPE;
+  if (!linear_shape(rows, in_features, out_features, fp8, gated)) return MHC_ERR_UNSUPPORTED_SHAPE;
   if (activation < MHC_ACT_NONE || activation > MHC_ACT_SWIGLU) return MHC_ERR_INVALID_ARG;
   if (!x || !weight || !out || (x_scale != nullptr) != fp8) return MHC_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(weight, 16) || !aligned(x_scale, 16) || !aligned(weight_scale, 16) ||
@@ -1116,11 +1140,7 @@ mhc_status mhc_linear(const void* x, const uint8_t* x_scale, int64_t x_stride, c
   if (static_cast<const void*>(residual) == out && (out_fp32 || residual_stride != out_stride))
     return MHC_ERR_INVALID_ARG;
   if (!workspace || !aligned(workspace, 256) || ws_bytes < mhc_linear_workspace_bytes(rows)) return MHC_ERR_WORKSPACE;
-  GemmParams p{};
-  p.rows = rows;
-  p.n = out_features;
-  p.kblocks = fp8 ? (in_features + 127) / 128 : (in_features + 63) / 64;
-  p.m_tiles = (out_features + kTileM - 1) / kTileM;
+  GemmParams p = linear_sizes(rows, in_features, out_features, fp8);
   p.x_scale = x_scale;
   p.w_scale = weight_scale;
   p.bias = bias;

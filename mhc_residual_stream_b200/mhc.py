@@ -129,6 +129,7 @@ def lib() -> ctypes.CDLL:
         "mhc_projection_pack_bytes": (_sz, [_i, _i]),
         "mhc_projection_pack": (_i, [_vp, _vp, _i, _i, _vp]),
         "mhc_linear_workspace_bytes": (_sz, [_i]),
+        "mhc_debug_linear_form": (_i, [_i, _i, _i, _i, _i, _vp]),
         "mhc_linear": (_i, [_vp, _vp, _i64, _vp, _vp, _vp, _i, _vp, _i64, _vp, _i, _i64, _i, _i, _i, _i, _vp, _sz, _vp]),
         "mhc_moe_route_workspace_bytes": (_sz, [_i, _i, _i]),
         "mhc_moe_route": (_i, [_vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _vp, _sz, _vp]),
@@ -629,6 +630,14 @@ def mhc_linear(x, weight, out, bias=None, activation: str = "none", residual=Non
                           R, K, N, read_ahead, pws_, wsb, _raw_stream(stream, dev))
     if st:
         raise MhcError(st, "mhc_linear")
+
+
+def mhc_debug_linear_form(rows: int, in_features: int, out_features: int, mxfp8: bool = False, gated: bool = False):
+    """(pair, CTAs that divide a tile's K, CTAs per SM, token columns of a tile) that
+    mhc_linear takes for a product of these sizes."""
+    form = (ctypes.c_int * 4)()
+    _check(lib().mhc_debug_linear_form(rows, in_features, out_features, mxfp8, gated, form), "mhc_debug_linear_form")
+    return bool(form[0]), form[1], form[2], form[3]
 
 
 def mhc_moe_route_workspace_bytes(rows: int, experts: int, top_k: int) -> int:
