@@ -1183,7 +1183,9 @@ __global__ void __launch_bounds__(256) mxfp8_rows_kernel(const __nv_bfloat16* __
                                                           uint8_t* __restrict__ data, uint8_t* __restrict__ scale,
                                                           int swizzled) {
   // No early launch of the next kernel: what is quantized here may be the weight that
-  // a following mhc_linear reads ahead of its wait.
+  // a following mhc_linear reads ahead of its wait. Without / with an early launch, in a
+  // graph: these rows and an MXFP8 product of them 32 x 7168 -> 7168 17.7 / 17.6 us, 128 x 7168
+  // -> 1024 14.5 / 13.9, 1 x 7168 -> 512 10.5 / 10.3; 32 x 7168 quantized back to back 2.14 / 2.47.
   griddep_wait();
   const int lanes_per_row = H / 8;
   const int scols = H / 32;

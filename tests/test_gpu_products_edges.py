@@ -125,3 +125,32 @@ def test_waits_that_run_out_leave_nothing_in_flight(fp8, act, R, K, N, budget):
     assert M.mhc_get_device_status(good) == M.OK
     for k in (1, 3, 5):
         assert torch.equal(out[k], want)
+
+
+@pytest.mark.parametrize("R,N,K", [(24, 256, 512), (130, 300, 160), (1, 7168, 1024)])
+def test_a_weight_that_is_quantized_directly_before(R, N, K):
+    # the quantizer lets no kernel start early, so even a product that reads its weights ahead
+    # finds them (and the padding of their scales) written
+    g = gen(N)
+    ws_ = [bf((N, K), g, 0.1).to(DEV) for _ in range(8)]
+    x = bf((R, K), g).to(DEV)
+
+    def buffers(t):
+        return (torch.zeros(t.shape, dtype=torch.uint8, device=DEV),
+                torch.zeros(M.mhc_mxfp8_scale_bytes(*t.shape, True), dtype=torch.uint8, device=DEV))
+    xq, want, outs = buffers(x), [], [torch.zeros(R, N, dtype=torch.bfloat16, device=DEV) for _ in ws_]
+    M.mxfp8_quantize_rows(x, *xq, True)
+    ws = M.new_linear_workspace(R, DEV)
+    for w in ws_:
+        wq = buffers(w)
+        M.mxfp8_quantize_rows(w, *wq, True)
+        torch.cuda.synchronize()
+        want.append(run_linear((*xq, True), (*wq, True)))
+    wq = buffers(ws_[0])
+    torch.cuda.synchronize()
+    for w, out in zip(ws_, outs):  # one buffer, rewritten before every product
+        M.mxfp8_quantize_rows(w, *wq, True)
+        M.mhc_linear((*xq, True), (*wq, True), out, workspace=ws)
+    torch.cuda.synchronize()
+    for out, t in zip(outs, want):
+        assert torch.equal(out, t)
