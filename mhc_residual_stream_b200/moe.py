@@ -55,8 +55,14 @@ class MoeWeights:
 
         def w(*shape):
             return (torch.randn(*shape, generator=g) / math.sqrt(shape[-1])).to(torch.bfloat16).to(device)
+
+        def experts(*shape):  # one at a time: 64 of 4096 x 7168 are 7.5 GB in fp32
+            out = torch.empty(E, *shape, dtype=torch.bfloat16, device=device)
+            for e in range(E):
+                out[e] = w(*shape)
+            return out
         return cls(router=w(E, hidden), bias=(torch.randn(E, generator=g) * 0.05).to(device) if cfg.balance else None,
-                   w13=w(E, 2 * I, hidden), w2=w(E, hidden, I), shared13=w(2 * Sh, hidden), shared2=w(hidden, Sh))
+                   w13=experts(2 * I, hidden), w2=experts(hidden, I), shared13=w(2 * Sh, hidden), shared2=w(hidden, Sh))
 
 
 class MoeSublayer:
