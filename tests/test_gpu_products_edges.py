@@ -154,3 +154,20 @@ def test_a_weight_that_is_quantized_directly_before(R, N, K):
     torch.cuda.synchronize()
     for out, t in zip(outs, want):
         assert torch.equal(out, t)
+
+
+@pytest.mark.parametrize("R", [3, 130, 300])
+def test_mxfp8_rows_may_be_strided(R):
+    g = gen(R)
+    K, N = 160, 200
+    ops = []
+    for t in (bf((R, K), g), bf((N, K), g, 0.1)):
+        q = torch.empty(t.shape, dtype=torch.uint8, device=DEV)
+        s = torch.empty(M.mhc_mxfp8_scale_bytes(*t.shape, True), dtype=torch.uint8, device=DEV)
+        M.mxfp8_quantize_rows(t.to(DEV), q, s, True)
+        ops.append((q, s, True))
+    want = run_linear(*ops)
+    wide = torch.full((R, 256), 0x7f, dtype=torch.uint8, device=DEV)  # NaN around the rows
+    wide[:, 16:16 + K] = ops[0][0]
+    got = run_linear((wide[:, 16:16 + K], ops[0][1], True), ops[1])
+    assert torch.equal(got, want)
