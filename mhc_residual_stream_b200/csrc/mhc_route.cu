@@ -413,15 +413,23 @@ __device__ __forceinline__ void choose_row(const RouteParams& p, int row, int la
   float w = 0.f;
   const float most = warp_max(chosen);  // the largest chosen logit
   if (id >= 0) {
-    if (!p.softmax) w = 1.f / (1.f + expf(-chosen));
-    else if (any_inf) w = chosen == INFINITY ? 1.f : 0.f;
-    else w = expf(chosen - (p.renorm ? most : shift));  // renormalised: any shift gives the same
+    if (!p.softmax) {
+      // of a negative logit e^l / (1 + e^l): e^-l leaves fp32's range at -88.7. Renormalised,
+      // over the largest e^l (any factor gives the same), so that a weight underflows only
+      // where its share does.
+      const float t = expf(-fabsf(chosen));
+      w = (chosen >= 0.f ? 1.f : p.renorm && most < 0.f ? expf(chosen - most) : t) / (1.f + t);
+    } else if (any_inf) {
+      w = chosen == INFINITY ? 1.f : 0.f;
+    } else {
+      w = expf(chosen - (p.renorm ? most : shift));  // renormalised: any shift gives the same
+    }
     if (!p.renorm) w /= sum;
   }
   if (p.renorm) {
     float total = warp_sum(w);
-    if (!p.softmax && total < 1e-20f) {
-      // every chosen sigmoid is near or below fp32's range: the ratio in 64 bits, where
+    if (!p.softmax && most < -46.f) {
+      // scores of less than 1e-20, down to none in 64 bits: the ratio in 64 bits, where
       // the sigmoid of less than -46 is the exponential (1 + e^46 is e^46 to 2^-66), which
       // unlike 1 / e^-l reaches the subnormals
       const double d = id >= 0 ? exp(static_cast<double>(chosen)) : 0.0;

@@ -75,3 +75,20 @@ def test_weights_of_scores_that_only_subnormals_hold():
     # each score is off by half a spacing at most, the sum by k of them; one rounding to fp32
     assert np.all(np.abs(w - exact) <= (k + 1) * spacing + 2.0 ** -23 * exact + 2.0 ** -126)
     assert np.all(np.abs(ow - exact) <= (k + 1) * spacing + 2.0 ** -40)
+
+
+@pytest.mark.parametrize("top", [-45.0, -20.0, -1.0, 3.0])
+@pytest.mark.parametrize("renormalize", [False, True])
+def test_sigmoid_weights_far_below_the_largest(top, renormalize):
+    # all experts are chosen; scores down to e^-120 under a largest one of e^-45 or more: ratios
+    # that are ordinary fp32 numbers although e^120 and e^-120 are none
+    R, E = 60, 8
+    logits = top - 85.0 * torch.rand(R, E, generator=gen(int(top) + 99))
+    logits[:, 3] = top
+    got = run_route(logits.to(DEV), E, scoring="sigmoid", renormalize=renormalize, weight_scale=2.5)
+    ow, oids = O.moe_route(f64(logits), E, scoring="sigmoid", renormalize=renormalize, weight_scale=2.5)
+    assert np.array_equal(got[1].cpu().numpy(), oids)
+    # two exponentials (2 steps each) of arguments off by half a step of at most 130, two
+    # divisions, a sum of 8 and the scale; where the weight is subnormal, its spacing
+    rel = (40 + 4 * 130) * 2.0 ** -24
+    assert np.all(np.abs(f64(got[0]) - ow) <= rel * np.abs(ow) + 2.0 ** -126)
