@@ -337,7 +337,8 @@ MHC_API mhc_status mxfp8_quantize_rows(const mhc_bf16* x, int rows, int hidden,
  *   mhc_mxfp8_out, padding bytes zero (as the boundaries and mxfp8_quantize_rows
  *   write them). Accumulated in fp32; out is rounded once, to bf16, or fp32
  *   (out_fp32 != 0). bias fp32 and residual bf16 may be NULL.
- *   activation: MHC_ACT_NONE / RELU / SILU (v sigmoid(v)) / GELU (v Phi(v), exact);
+ *   activation: MHC_ACT_NONE / RELU / SILU (v sigmoid(v); 0 below -88.7, where it is
+ *   less than 3e-37 in magnitude) / GELU (v Phi(v), exact);
  *   MHC_ACT_SWIGLU: weight is [2 out, in] (bias [2 out]), gate rows first, and
  *   act = silu(gate) * up.
  *   Strides are in elements, between rows; x rows 16-byte aligned (x_stride a
@@ -470,9 +471,10 @@ MHC_API mhc_status mhc_get_device_status(void* workspace, mhc_stream stream);
 MHC_API const char* mhc_status_string(mhc_status status);
 
 /* Test hook for the bounded waits. A kernel waits on the TMA copies of its fn
- * slice (and the mailbox kernels on their slots and consumed words) with a time limit: `budget_ns`
- * > 0 sets it (default 1e9 ns, counted as
- * 2 SM cycles per ns); `extra_units` makes that wait expect that many 16-byte
+ * slice (the mailbox kernels on their slots and consumed words, mhc_linear and
+ * mhc_moe_experts on their copies and products) with a time limit: `budget_ns`
+ * > 0 sets it (default 1e9 ns, counted as 2 SM cycles per ns; in mhc_linear and
+ * mhc_moe_experts it is 1e5 ns at least); `extra_units` makes that wait expect that many 16-byte
  * units more than are copied, so that it can never complete and runs out
  * (recording MHC_ERR_DEVICE_TIMEOUT). Affects launches made after the call by
  * this process. Returns the previous budget. */

@@ -338,6 +338,7 @@ __device__ __forceinline__ void bulk_s2cluster(unsigned dst, unsigned src, unsig
       : "memory");
 }
 
+// Below -88.7 the exponential is infinite and the result 0 (the value is less than 3e-37 in magnitude).
 __device__ __forceinline__ float silu(float v) { return v / (1.f + __expf(-v)); }
 
 // C token columns of a warp's 32 output features (thread: feature f), from the
@@ -1106,8 +1107,9 @@ extern "C" {
 
 mhc_status mhc_debug_linear_form(int rows, int in_features, int out_features, int mxfp8, int gated, int* form) {
   if (!form) return MHC_ERR_INVALID_ARG;
-  if (!linear_shape(rows, in_features, out_features, mxfp8 != 0, gated != 0)) return MHC_ERR_UNSUPPORTED_SHAPE;
-  const Plan plan = plan_linear(linear_sizes(rows, in_features, out_features, mxfp8 != 0), rows, mxfp8 != 0, gated != 0);
+  const bool fp8 = mxfp8 != 0;
+  if (!linear_shape(rows, in_features, out_features, fp8, gated != 0)) return MHC_ERR_UNSUPPORTED_SHAPE;
+  const Plan plan = plan_linear(linear_sizes(rows, in_features, out_features, fp8), rows, fp8, gated != 0);
   form[0] = plan.pair;
   form[1] = plan.split;
   form[2] = plan.per_sm;
@@ -1233,7 +1235,7 @@ mhc_status mhc_moe_experts(const mhc_bf16* x, int64_t x_stride, const mhc_bf16* 
   p.n = intermediate;
   p.kblocks = (hidden + 63) / 64;
   p.m_tiles = (intermediate + kTileM - 1) / kTileM;
-  p.out = inner;
+  p.out = inner;  // in bf16, the tensor cores' operand type: each value is off by 2^-8 of itself at most
   p.out_stride = intermediate;
   p.act = MHC_ACT_SWIGLU;
   if (!make_map2(&mw, w13, false, hidden, static_cast<uint64_t>(experts) * 2 * intermediate,
