@@ -1,6 +1,5 @@
 """GPU test of a product in each form of mhc_linear that the sublayer tests do not reach."""
 
-import numpy as np
 import pytest
 import torch
 

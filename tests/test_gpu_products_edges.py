@@ -1,11 +1,9 @@
 """GPU tests of mhc_linear and mhc_moe_experts beside their sizes and types: one
 workspace for several operators, tiles that several CTAs share."""
 
-import numpy as np
 import pytest
 import torch
 
-import oracle as O
 from mhc_residual_stream_b200 import mhc as M
 
 from _sublayer import (DEV, assert_within, bf, draw_experts, experts_bound, f64, gen, i32, run_linear, run_route)

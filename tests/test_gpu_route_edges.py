@@ -1,8 +1,6 @@
 """GPU tests of mhc_moe_route where its fp32 choices and the 64-bit definition part:
 groups whose values carry unlike errors or leave fp32's range, scores below it."""
 
-import math
-
 import numpy as np
 import pytest
 import torch
